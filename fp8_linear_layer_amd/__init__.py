@@ -487,3 +487,8 @@ def te_fp8_wgrad_accum_bgrad(a, a_scales, a_dtype, b, b_scales, b_dtype, out, bi
         _ptr(a), _ptr(a_scales), a_dtype, _ptr(b), _ptr(b_scales), b_dtype, M, N, K, _ptr(out), out.stride(0),
         _ptr(bias_grad), accum, _stream(stream)))
     return out
+
+
+# the operators around the GEMMs (include/te_ops.h)
+from .ops import (RmsNormOutput, RouterOutput, te_grad_norm_clip, te_moe_router_bwd, te_moe_router_fwd,  # noqa: E402,F401
+                  te_rmsnorm_bwd, te_rmsnorm_fwd)

@@ -13,7 +13,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libte_fp8.so")
 # (source, object, extra flags): gemm.hip is compiled once per operand-format pair and once for its
 # host side (TE_GEMM_PART), so its kernel instantiations build in parallel
-SOURCES = [("api.cpp", "api.o", []), ("cast.hip", "cast.o", [])] + \
+SOURCES = [("api.cpp", "api.o", []), ("api_ops.cpp", "api_ops.o", []), ("cast.hip", "cast.o", []),
+           ("norm.hip", "norm.o", []), ("router.hip", "router.o", []), ("grad_clip.hip", "grad_clip.o", [])] + \
     [("gemm.hip", f"gemm_p{i}.o", [f"-DTE_GEMM_PART={i}"]) for i in range(9)]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "ops_internal.h"
 #include "te_fp8.h"
 
 namespace {
@@ -134,6 +135,20 @@ te_status_t launch(const char* fn, const tefp8::GemmArgs& g, hipStream_t stream,
 }
 
 }  // namespace
+
+namespace tefp8 {
+te_status_t report(te_status_t status, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(status, "%s", buf);
+}
+te_status_t report_ok() { return ok(); }
+bool log_calls() { return log_enabled(); }
+}  // namespace tefp8
 
 extern "C" {
 
