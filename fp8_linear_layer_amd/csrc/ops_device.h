@@ -46,28 +46,66 @@ __device__ __forceinline__ Raw8<F32> load8(const float* p)
 {
     return {*reinterpret_cast<const u32x4_a4*>(p), *reinterpret_cast<const u32x4_a4*>(p + 4)};
 }
-// n < 8 elements, zeros behind them.
-__device__ __forceinline__ Raw8<Bf16> load_few(const uint16_t* p, int n)
+// n < 8 elements, and behind them `fill` (the bits of an fp32 number that bf16 holds too).
+__device__ __forceinline__ Raw8<Bf16> load_few(const uint16_t* p, int n, uint32_t fill = 0)
 {
     Raw8<Bf16> r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
+        const uint32_t lo = 2 * i < n ? p[2 * i] : fill >> 16, hi = 2 * i + 1 < n ? p[2 * i + 1] : fill >> 16;
         r.a[i] = lo | hi << 16;
     }
     return r;
 }
-__device__ __forceinline__ Raw8<F32> load_few(const float* p, int n)
+__device__ __forceinline__ Raw8<F32> load_few(const float* p, int n, uint32_t fill = 0)
 {
     Raw8<F32> r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        r.a[i] = i < n ? as_bits(p[i]) : 0;
-        r.b[i] = 4 + i < n ? as_bits(p[4 + i]) : 0;
+        r.a[i] = i < n ? as_bits(p[i]) : fill;
+        r.b[i] = 4 + i < n ? as_bits(p[4 + i]) : fill;
+    }
+    return r;
+}
+// Elements n .. 7 to the front, and `fill` behind them (0 <= n < 8).
+__device__ __forceinline__ Raw8<Bf16> drop_front(Raw8<Bf16> r, int n, uint32_t fill)
+{
+    const uint32_t f = fill | fill >> 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t next = i < 3 ? (uint32_t)r.a[i + 1 & 3] : f;
+        r.a[i] = n & 1 ? r.a[i] >> 16 | next << 16 : (uint32_t)r.a[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.a[i] = n & 2 ? (i < 3 ? (uint32_t)r.a[i + 1 & 3] : f) : (uint32_t)r.a[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.a[i] = n & 4 ? (i < 2 ? (uint32_t)r.a[i + 2 & 3] : f) : (uint32_t)r.a[i];
+    return r;
+}
+__device__ __forceinline__ Raw8<F32> drop_front(Raw8<F32> r, int n, uint32_t fill)
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = i < 4 ? (uint32_t)r.a[i & 3] : (uint32_t)r.b[i & 3];
+#pragma unroll
+    for (int s = 1; s <= 4; s *= 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = n & s ? (i + s < 8 ? w[i + s & 7] : fill) : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r.a[i] = w[i];
+        r.b[i] = w[4 + i];
     }
     return r;
 }
 template <class T> __device__ __forceinline__ Raw8<T> zero8();
+template <class T> __device__ __forceinline__ Raw8<T> fill8(uint32_t fill);
+template <> __device__ __forceinline__ Raw8<Bf16> fill8<Bf16>(uint32_t f)
+{
+    f |= f >> 16;
+    return {u32x4_t{f, f, f, f}};
+}
+template <> __device__ __forceinline__ Raw8<F32> fill8<F32>(uint32_t f) { return {u32x4_t{f, f, f, f}, u32x4_t{f, f, f, f}}; }
 template <> __device__ __forceinline__ Raw8<Bf16> zero8<Bf16>() { return {u32x4_t{0, 0, 0, 0}}; }
 template <> __device__ __forceinline__ Raw8<F32> zero8<F32>() { return {u32x4_t{0, 0, 0, 0}, u32x4_t{0, 0, 0, 0}}; }
 
@@ -128,7 +166,8 @@ __device__ __forceinline__ void store_few(P* p, const R& r, int n)   // n < 8
 template <int kCtrl>
 __device__ __forceinline__ int dpp(int v)
 {
-    return __builtin_amdgcn_mov_dpp(v, kCtrl, 0xF, 0xF, false);
+    // (every lane's source is inside its row; said this way the exchange folds into the instruction that uses it)
+    return __builtin_amdgcn_update_dpp(0, v, kCtrl, 0xF, 0xF, true);
 }
 // The value of a partner lane in the other half of the aligned group of 2 * kStep lanes, for
 // values that are already equal over each aligned group of kStep lanes.

@@ -24,92 +24,113 @@
 
 #include <algorithm>
 
+#include "internal.h"
 #include "ops_device.h"
 #include "ops_internal.h"
 
 namespace tefp8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr uint32_t kNegInf = 0xFF800000u;
-constexpr uint32_t kClosed = 0x007FFFFFu;   // order-preserving bits of -inf: nothing at or below is chosen
-constexpr uint32_t kOpenInf = 0xFF800000u;  // ... of +inf: NaN lies above
 
-// Order-preserving bits: unsigned comparison of the results is comparison of the floats (-0 = +0).
-__device__ __forceinline__ uint32_t order_bits(float v)
+// Signed integers in the order of the floats: the magnitude's bits, negated for negative numbers
+// (so -0 = +0).  -inf is kClosed: nothing at or below is chosen; NaN lies above +inf or below -inf.
+constexpr int32_t kOpenInf = 0x7F800000, kClosed = -kOpenInf;
+__device__ __forceinline__ int32_t order_key(uint32_t bits)
 {
-    const uint32_t b = as_bits(v + 0.0f);
-    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    const int32_t neg = (int32_t)bits >> 31;
+    return ((int32_t)(bits & 0x7FFFFFFFu) ^ neg) - neg;
 }
-__device__ __forceinline__ float from_order_bits(uint32_t k)
+__device__ __forceinline__ float from_order_key(int32_t k)
 {
-    return as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+    return as_float(k < 0 ? (uint32_t)-k | 0x80000000u : (uint32_t)k);
 }
-__device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t x)   // a >= b
+// The middle one; written so that it becomes one instruction.
+__device__ __forceinline__ int32_t med3(int32_t a, int32_t b, int32_t x) { return max(min(a, b), min(max(a, b), x)); }
+
+// exp for arguments at or below zero: one product and the hardware's exp2, off by about |x| 2^-24 of
+// the value, which the sums and the bf16 results here do not feel (a term that is far down weighs little) ...
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+// ... and with the product's rounding, and log2(e)'s, carried along, for the fp32 results.  (The
+// bound keeps the correction finite where the result is zero; it drops a NaN.)
+__device__ __forceinline__ float exp_exact(float x)
 {
-    return max(min(a, x), b);
+    x = fmaxf(x, -1e30f);
+    const float t = x * 1.44269504f;
+    const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, r * 0.693147181f, e);
 }
 
 // A sorted list of the kK largest (key, column), equal keys by the lower column.
 template <class T, int kK> struct TopList;
 
 template <int kK> struct TopList<Bf16, kK> {
-    uint32_t a[kK];
+    int32_t a[kK];   // the upper half of the key, and below it what makes equal keys differ
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int j = 0; j < kK; ++j) a[j] = 0;
+        for (int j = 0; j < kK; ++j) a[j] = INT32_MIN;
     }
-    // `pos` counts the lane's own elements (0 .. 63), in ascending column order
-    __device__ __forceinline__ void insert(uint32_t key, int pos)
+    __device__ __forceinline__ void insert(int32_t x)
     {
-        const uint32_t x = (key & 0xFFFF0000u) | (63 - pos);
 #pragma unroll
         for (int j = kK - 1; j > 0; --j) a[j] = med3(a[j - 1], a[j], x);
         a[0] = max(a[0], x);
     }
-    // own positions -> columns
+    // Eight logits; the lane's own elements are numbered from `pos` on, in ascending column order (0 .. 63).
+    __device__ __forceinline__ void insert8(const Raw8<Bf16>& r, int pos, bool drop_nan)
+    {
+        typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = r.a[i], m = w & 0x7FFF7FFFu;
+            const i16x2 neg = __builtin_bit_cast(i16x2, w) >> 15;
+            uint32_t k = __builtin_bit_cast(uint32_t, (__builtin_bit_cast(i16x2, m) ^ neg) - neg);
+            if (drop_nan) {
+                if ((m & 0xFFFFu) > 0x7F80u) k = (k & 0xFFFF0000u) | 0x8000u;
+                if (m >> 16 > 0x7F80u) k = (k & 0xFFFFu) | 0x80000000u;
+            }
+            insert((int32_t)((k << 16) | (63 - (pos + 2 * i))));
+            insert((int32_t)((k & 0xFFFF0000u) | (63 - (pos + 2 * i + 1))));
+        }
+    }
+    // own numbers -> columns
     template <class F> __device__ __forceinline__ void to_columns(F column)
     {
 #pragma unroll
-        for (int j = 0; j < kK; ++j) a[j] = (a[j] & 0xFFFF0000u) | (0xFFFF - column(63 - (int)(a[j] & 63)));
+        for (int j = 0; j < kK; ++j) a[j] = (a[j] & (int32_t)0xFFFF0000) | (0xFFFF - column(63 - (a[j] & 63)));
     }
-    // (the order bits of a negative bf16 end in sixteen ones, which the column's bits replaced)
-    __device__ __forceinline__ uint32_t key(int j) const
-    {
-        const uint32_t k = a[j] & 0xFFFF0000u;
-        return (int32_t)k < 0 ? k : k | 0xFFFFu;
-    }
-    __device__ __forceinline__ int column(int j) const { return 0xFFFF - (int)(a[j] & 0xFFFFu); }
+    __device__ __forceinline__ int32_t key(int j) const { return a[j] & (int32_t)0xFFFF0000; }
+    __device__ __forceinline__ int column(int j) const { return 0xFFFF - (a[j] & 0xFFFF); }
     template <int kStep> __device__ __forceinline__ void take_partner()
     {
-        uint32_t b[kK];
+        int32_t b[kK];
 #pragma unroll
-        for (int j = 0; j < kK; ++j) b[j] = (uint32_t)partner<kStep>((int)a[kK - 1 - j]);
+        for (int j = 0; j < kK; ++j) b[j] = max(a[j], partner<kStep>(a[kK - 1 - j]));
 #pragma unroll
-        for (int j = 0; j < kK; ++j) a[j] = max(a[j], b[j]);
+        for (int j = 0; j < kK; ++j) a[j] = b[j];
     }
     __device__ __forceinline__ void order(int i, int j)
     {
-        const uint32_t hi = max(a[i], a[j]), lo = min(a[i], a[j]);
+        const int32_t hi = max(a[i], a[j]), lo = min(a[i], a[j]);
         a[i] = hi;
         a[j] = lo;
     }
 };
 
 template <int kK> struct TopList<F32, kK> {
-    uint32_t a[kK];
+    int32_t a[kK];
     int c[kK];
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
         for (int j = 0; j < kK; ++j) {
-            a[j] = 0;
-            c[j] = 0x7FFFFFFF;
+            a[j] = INT32_MIN;
+            c[j] = 0;
         }
     }
-    __device__ __forceinline__ void insert(uint32_t x, int pos)
+    __device__ __forceinline__ void insert(int32_t x, int pos)
     {
         bool above = x > a[kK - 1];   // x goes above entry j (an equal earlier one stays above x)
 #pragma unroll
@@ -122,24 +143,34 @@ template <int kK> struct TopList<F32, kK> {
         c[0] = above ? pos : c[0];
         a[0] = max(a[0], x);
     }
+    __device__ __forceinline__ void insert8(const Raw8<F32>& r, int pos, bool drop_nan)
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w = j < 4 ? (uint32_t)r.a[j & 3] : (uint32_t)r.b[j & 3];
+            int32_t k = order_key(w);
+            if (drop_nan && (w & 0x7FFFFFFFu) > 0x7F800000u) k = INT32_MIN;
+            insert(k, pos + j);
+        }
+    }
     template <class F> __device__ __forceinline__ void to_columns(F column)
     {
 #pragma unroll
-        for (int j = 0; j < kK; ++j) c[j] = c[j] == 0x7FFFFFFF ? c[j] : column(c[j]);
+        for (int j = 0; j < kK; ++j) c[j] = column(c[j]);
     }
-    __device__ __forceinline__ uint32_t key(int j) const { return a[j]; }
+    __device__ __forceinline__ int32_t key(int j) const { return a[j]; }
     __device__ __forceinline__ int column(int j) const { return c[j]; }
-    static __device__ __forceinline__ bool before(uint32_t ka, int ca, uint32_t kb, int cb)
+    static __device__ __forceinline__ bool before(int32_t ka, int ca, int32_t kb, int cb)
     {
         return ka > kb || (ka == kb && ca < cb);
     }
     template <int kStep> __device__ __forceinline__ void take_partner()
     {
-        uint32_t b[kK];
+        int32_t b[kK];
         int d[kK];
 #pragma unroll
         for (int j = 0; j < kK; ++j) {
-            b[j] = (uint32_t)partner<kStep>((int)a[kK - 1 - j]);
+            b[j] = partner<kStep>(a[kK - 1 - j]);
             d[j] = partner<kStep>(c[kK - 1 - j]);
         }
 #pragma unroll
@@ -152,7 +183,7 @@ template <int kK> struct TopList<F32, kK> {
     __device__ __forceinline__ void order(int i, int j)
     {
         const bool keep = before(a[i], c[i], a[j], c[j]);
-        const uint32_t ka = a[i];
+        const int32_t ka = a[i];
         const int ca = c[i];
         a[i] = keep ? ka : a[j];
         c[i] = keep ? ca : c[j];
@@ -182,33 +213,15 @@ __device__ __forceinline__ void merge_lanes(TopList<T, kK>& l)
     if constexpr (kL > 32) merge<32>(l);
 }
 
-// Where the chunk with nominal first column `col` is loaded from: the last one of a row whose
-// length is no multiple of eight starts at experts - 8 and shares its first columns with its
-// neighbour.
-__device__ __forceinline__ int chunk_start(int col, int experts) { return max(min(col, experts - 8), 0); }
-
-__device__ __forceinline__ void set_raw(Raw8<Bf16>& r, int j, uint32_t bits)
+// The eight logits from column `col` on; columns past the last read as -inf.  (The last chunk of a row
+// whose length is no multiple of eight is loaded from experts - 8 and moved to the front.)
+template <class T, bool kFew, class P>
+__device__ __forceinline__ Raw8<T> load_logits(const P* row, int col, int experts)
 {
-    r.a[j >> 1] = (j & 1) ? (r.a[j >> 1] & 0xFFFFu) | (bits & 0xFFFF0000u) : (r.a[j >> 1] & 0xFFFF0000u) | bits >> 16;
-}
-__device__ __forceinline__ void set_raw(Raw8<F32>& r, int j, uint32_t bits)
-{
-    if (j < 4) r.a[j & 3] = bits;
-    else r.b[j & 3] = bits;
-}
-// Eight logits; those that are no columns of this chunk read as -inf.
-template <class T, class P>
-__device__ __forceinline__ Raw8<T> load_logits(const P* row, int col, int experts, bool live)
-{
-    const int c0 = chunk_start(col, experts);
-    Raw8<T> r = zero8<T>();
-    if (live && col < experts) r = experts < 8 ? load_few(row, experts) : load8(row + c0);
-    const int lo = live ? col - c0 : 8, hi = experts - c0;   // columns lo .. hi - 1 are the chunk's own
-    if (lo > 0 || hi < 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < lo || j >= hi) set_raw(r, j, kNegInf);
-    }
+    if (kFew && experts < 8) return load_few(row, experts, kNegInf);
+    const int c0 = min(col, experts - 8);
+    Raw8<T> r = load8(row + c0);
+    if (col != c0) r = col < experts ? drop_front(r, col - c0, kNegInf) : fill8<T>(kNegInf);
     return r;
 }
 
@@ -251,13 +264,21 @@ __device__ __forceinline__ double block_sum(double v, double* red)
     return s;
 }
 
+constexpr int kFwdThreads = 512;
+constexpr int kFwdWaves = kFwdThreads / 64;
+
+// (Waves per SIMD that the registers are cut for: four take 128 each, which the long lists and the rows of
+// fp32 do not fit.)
+template <class T, int kNC, int kK> constexpr int kFwdWavesPerSimd = kK == 16 || (kNC == 4 && __is_same(T, F32)) ? 2 : 4;
+
 template <class T, int kL, int kNC, int kK, bool kLoss>
-__global__ __launch_bounds__(kThreads) void router_fwd_kernel(const RouterArgs a)
+__global__ __launch_bounds__(kFwdThreads, (kFwdWavesPerSimd<T, kNC, kK>)) void router_fwd_kernel(const RouterArgs a)
 {
-    extern __shared__ int32_t lds[];   // with the loss: counts [experts], sums of p [kWaves][experts]
+    extern __shared__ int32_t lds[];   // with the loss: counts [experts], sums of p [kFwdWaves][experts]
     __shared__ int32_t routed;
-    __shared__ double red[kWaves];
+    __shared__ double red[kFwdWaves];
     constexpr int kRows = 64 / kL;     // tokens per wave and step
+    constexpr bool kAhead = kNC <= 2;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int p = lane % kL, slot = lane / kL;
     const int E = a.experts, k = a.top_k;
@@ -268,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void router_fwd_kernel(const RouterArgs a
     float acc[kNC][8];
     int n_routed = 0;
     if constexpr (kLoss) {
-        for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+        for (int e = threadIdx.x; e < E; e += kFwdThreads) hist[e] = 0;
         if (threadIdx.x == 0) {
             routed = 0;
             // (for the second kernel, which starts after this one has ended)
@@ -281,37 +302,45 @@ __global__ __launch_bounds__(kThreads) void router_fwd_kernel(const RouterArgs a
             for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
     }
 
-    const int64_t step = (int64_t)gridDim.x * kWaves * kRows;
-    for (int64_t base = ((int64_t)blockIdx.x * kWaves + wave) * kRows; base < a.tokens; base += step) {
-        const int64_t t = base + slot;
-        bool live = t < a.tokens;
-        if (live && a.mask) live = a.mask[t] != 0;
+    const int64_t step = (int64_t)gridDim.x * kFwdWaves * kRows;
+    int64_t base = ((int64_t)blockIdx.x * kFwdWaves + wave) * kRows;
+    // Tokens past the end repeat the last one and store nothing.
+    Raw8<T> raw[kNC], next[kNC];
+    uint8_t unmasked = 1, next_unmasked = 1;
+    auto fetch = [&](int64_t b, Raw8<T> (&r)[kNC], uint8_t& m) {
+        const int64_t t = min(b + slot, a.tokens - 1);
         const auto* row = logits + t * a.ld;
-        Raw8<T> raw[kNC];
+        if (a.mask) m = a.mask[t];
 #pragma unroll
-        for (int i = 0; i < kNC; ++i) raw[i] = load_logits<T>(row, (i * kL + p) * 8, E, live);
+        for (int i = 0; i < kNC; ++i) r[i] = load_logits<T, kL * kNC == 1>(row, (i * kL + p) * 8, E);
+    };
+    if (kAhead && base < a.tokens) fetch(base, next, next_unmasked);
+    for (; base < a.tokens; base += step) {
+        const int64_t t = base + slot;
+        if constexpr (kAhead) {
+            unmasked = next_unmasked;
+#pragma unroll
+            for (int i = 0; i < kNC; ++i) raw[i] = next[i];
+            if (base + step < a.tokens) fetch(base + step, next, next_unmasked);
+        } else {
+            fetch(base, raw, unmasked);
+        }
+        const bool in = t < a.tokens, live = in && unmasked != 0;
 
         TopList<T, kK> top;
         auto select = [&](bool drop_nan) {
             top.clear();
 #pragma unroll
-            for (int i = 0; i < kNC; ++i) {
-                float v[8];
-                unpack8(raw[i], v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint32_t key = order_bits(v[j]);
-                    if (drop_nan) key = key > kOpenInf ? 0 : key;
-                    top.insert(key, i * 8 + j);
-                }
-            }
-            top.to_columns([&](int pos) { return chunk_start(((pos >> 3) * kL + p) * 8, E) + (pos & 7); });
+            for (int i = 0; i < kNC; ++i) top.insert8(raw[i], i * 8, drop_nan);
+            top.to_columns([&](int pos) { return ((pos >> 3) * kL + p) * 8 + (pos & 7); });
             merge_lanes<kL>(top);
         };
         select(false);
+        // A NaN above all others was chosen: choose again without any (those below -inf never are).  The
+        // sum of the row is NaN in both cases, and with it the token's weights.
+        if (__any(top.key(0) > kOpenInf)) select(true);
 
-        const bool open = top.key(0) > kClosed;
-        const float m = open ? from_order_bits(top.key(0)) : 0.0f;
+        const float m = top.key(0) > kClosed ? from_order_key(top.key(0)) : 0.0f;
         float s = 0.0f;
         float e[kNC][8];
 #pragma unroll
@@ -320,45 +349,45 @@ __global__ __launch_bounds__(kThreads) void router_fwd_kernel(const RouterArgs a
             unpack8(raw[i], v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                e[i][j] = __expf(v[j] - m);
+                e[i][j] = exp_fast(v[j] - m);
                 s += e[i][j];
             }
         }
         s = sum_lanes<kL>(s);
-        // A NaN logit sorts above all others: choose again without it (its weights stay NaN).
-        if (__any(s != s)) select(true);
         const bool sent = live && top.key(0) > kClosed;
 
+        // lane p has entries p, p + kL, ...
+        constexpr int kOwn = (kK + kL - 1) / kL;
+        float ev[kOwn], sum = 0.0f;
+        int col[kOwn];
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q) {
+            int32_t key = top.key(q * kL);
+            col[q] = top.column(q * kL);
+#pragma unroll
+            for (int i = 1; i < kL && q * kL + i < kK; ++i) {
+                key = p == i ? top.key(q * kL + i) : key;
+                col[q] = p == i ? top.column(q * kL + i) : col[q];
+            }
+            const bool chosen = sent && key > kClosed && q * kL + p < min(k, kK);
+            ev[q] = chosen ? expf(from_order_key(key) - m) : 0.0f;
+            if (!chosen) col[q] = -1;
+            sum += ev[q];
+        }
         const float inv = 1.0f / s;
         float scale = inv;
-        if (a.renorm) {
-            float w = 0.0f;
+        if (a.renorm) scale = s == s ? 1.0f / sum_lanes<kL>(sum) : s;
 #pragma unroll
-            for (int j = 0; j < kK; ++j)
-                if (j < k && top.key(j) > kClosed) w += expf(from_order_bits(top.key(j)) - m);
-            scale = 1.0f / w;
-            if (s != s) scale = s;
-        }
-        // lane p writes entries p, p + kL, ...
-#pragma unroll
-        for (int j0 = 0; j0 < kK; j0 += kL) {
-            uint32_t key = top.key(j0);
-            int col = top.column(j0);
-#pragma unroll
-            for (int q = 1; q < kL && j0 + q < kK; ++q) {
-                key = p == q ? top.key(j0 + q) : key;
-                col = p == q ? top.column(j0 + q) : col;
-            }
-            const int j = j0 + p;
-            if (j < k && p + j0 < kK && t < a.tokens) {
-                const bool chosen = sent && key > kClosed;
-                a.index[t * k + j] = chosen ? col : -1;
-                a.weight[t * k + j] = chosen ? expf(from_order_bits(key) - m) * scale : 0.0f;
+        for (int q = 0; q < kOwn; ++q) {
+            const int j = q * kL + p;
+            if (in && j < k && j < kK) {
+                a.index[t * k + j] = col[q];
+                a.weight[t * k + j] = col[q] >= 0 ? ev[q] * scale : 0.0f;
                 if constexpr (kLoss)
-                    if (chosen) atomicAdd(&hist[col], 1);
+                    if (col[q] >= 0) atomicAdd(&hist[col[q]], 1);
             }
         }
-        if (a.lse && p == 0 && t < a.tokens) a.lse[t] = sent ? m + logf(s) : 0.0f;
+        if (a.lse && p == 0 && in) a.lse[t] = sent ? m + logf(s) : 0.0f;
         if constexpr (kLoss) {
             if (sent) {
                 n_routed += p == 0;
@@ -371,33 +400,56 @@ __global__ __launch_bounds__(kThreads) void router_fwd_kernel(const RouterArgs a
     }
 
     if constexpr (kLoss) {
-        // the wave's tokens side by side (lanes p, p + kL, ...), then the waves
+        // The wave's tokens side by side (lanes p, p + kL, ...): the halves and the rows of the wave
+        // exchange, so that each keeps half of the sums, then the lanes of a row.
+        float v[kNC * 8];
+        int n = kNC * 8, first = 0;
 #pragma unroll
-        for (int i = 0; i < kNC; ++i) {
-            const int col = (i * kL + p) * 8, c0 = chunk_start(col, E);
+        for (int i = 0; i < kNC * 8; ++i) v[i] = acc[i >> 3][i & 7];
+        if constexpr (kL <= 32) {
+            n /= 2;
+            first += (lane & 32) ? n : 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int s = kL; s < 64; s <<= 1) acc[i][j] += __shfl_xor(acc[i][j], s);
-                if (slot == 0 && c0 + j >= col && c0 + j < E) sums[wave * E + c0 + j] = acc[i][j];
+            for (int i = 0; i < kNC * 4; ++i) {
+                const auto x = __builtin_amdgcn_permlane32_swap(as_bits(v[i]), as_bits(v[i + kNC * 4]), false, false);
+                v[i] = as_float(x[0]) + as_float(x[1]);
             }
+        }
+        if constexpr (kL <= 16) {
+            n /= 2;
+            first += (lane & 16) ? n : 0;
+#pragma unroll
+            for (int i = 0; i < kNC * 2; ++i) {
+                const auto x = __builtin_amdgcn_permlane16_swap(as_bits(v[i]), as_bits(v[i + kNC * 2]), false, false);
+                v[i] = as_float(x[0]) + as_float(x[1]);
+            }
+        }
+        constexpr int kKept = kNC * 8 / (kL <= 16 ? 4 : kL <= 32 ? 2 : 1);
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) {
+            if constexpr (kL <= 8) v[i] += as_float((uint32_t)dpp<0x128>((int)as_bits(v[i])));   // row_ror:8
+            if constexpr (kL <= 4) v[i] += as_float((uint32_t)dpp<0x124>((int)as_bits(v[i])));
+            if constexpr (kL <= 2) v[i] += as_float((uint32_t)dpp<0x122>((int)as_bits(v[i])));
+            if constexpr (kL <= 1) v[i] += as_float((uint32_t)dpp<0x121>((int)as_bits(v[i])));
+            const int f = first + i, col = ((f >> 3) * kL + p) * 8 + (f & 7);
+            if ((lane & 15) < kL && col < E) sums[wave * E + col] = v[i];
         }
         if (n_routed) atomicAdd(&routed, n_routed);
         __syncthreads();
         if (a.workspace) {
             const Space w = space_at(a.workspace, a.blocks, E);
-            for (int e = threadIdx.x; e < E; e += kThreads) {
+            for (int e = threadIdx.x; e < E; e += kFwdThreads) {
                 float s = 0.0f;
-                for (int q = 0; q < kWaves; ++q) s += sums[q * E + e];
+                for (int q = 0; q < kFwdWaves; ++q) s += sums[q * E + e];
                 w.counts[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
                 w.probs[(int64_t)blockIdx.x * E + e] = s;
             }
             if (threadIdx.x == 0) w.counts[(int64_t)blockIdx.x * (E + 1) + E] = routed;
         } else {
             double part = 0.0;
-            for (int e = threadIdx.x; e < E; e += kThreads) {
+            for (int e = threadIdx.x; e < E; e += kFwdThreads) {
                 double s = 0.0;
-                for (int q = 0; q < kWaves; ++q) s += (double)sums[q * E + e];
+                for (int q = 0; q < kFwdWaves; ++q) s += (double)sums[q * E + e];
                 a.counts[e] = hist[e];
                 part += (double)hist[e] * s;
             }
@@ -415,15 +467,15 @@ __global__ __launch_bounds__(kThreads) void router_fwd_kernel(const RouterArgs a
 __global__ __launch_bounds__(1024) void router_finish_kernel(const RouterArgs a)
 {
     __shared__ double red_p[16][kFinishCols];
-    __shared__ int64_t red_c[16][kFinishCols];
+    __shared__ int32_t red_c[16][kFinishCols];
     __shared__ double part[kFinishCols];
     const int E = a.experts, cl = threadIdx.x % kFinishCols, rl = threadIdx.x / kFinishCols;
     const int e = blockIdx.x * kFinishCols + cl;
     const Space w = space_at(a.workspace, a.blocks, E);
     double s = 0.0;
-    int64_t c = 0;
+    int32_t c = 0;
     if (e <= E) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t b = rl; b < a.blocks; b += 1024 / kFinishCols) {
             c += w.counts[b * (E + 1) + e];
             if (e < E) s += (double)w.probs[b * E + e];
@@ -447,25 +499,35 @@ __global__ __launch_bounds__(1024) void router_finish_kernel(const RouterArgs a)
             s += red_p[i][cl];
             c += red_c[i][cl];
         }
-        if (e < E) a.counts[e] = (int32_t)c;
-        else if (e == E) __hip_atomic_store(a.routed, (int32_t)c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (e < E) a.counts[e] = c;
+        else if (e == E) __hip_atomic_store(a.routed, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         part[cl] = e < E ? (double)c * s : 0.0;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double v = 0.0;
-        for (int i = 0; i < kFinishCols; ++i) v += part[i];
-        __hip_atomic_store(&w.sums[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        if (__hip_atomic_fetch_add(w.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1) {
-            double v = 0.0;
-            for (int i = 0; i < (int)gridDim.x; ++i)
-                v += __hip_atomic_load(&w.sums[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const int32_t n = __hip_atomic_load(a.routed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            a.loss[0] = balance_loss(v, n, E, a.top_k);
+    if (threadIdx.x >= 64) return;
+    double v = 0.0;
+    for (int i = 0; i < kFinishCols; ++i) v += part[i];
+    if (gridDim.x > 1) {
+        // What the last workgroup reads of the others (this sum, and `routed`, stored above by this wave)
+        // goes to memory by agent-wide stores; waiting for them is all the order that is needed, and a
+        // release would write the whole L2 back.
+        int32_t before = 0;
+        if (threadIdx.x == 0) {
+            __hip_atomic_store(&w.sums[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            before = __hip_atomic_fetch_add(w.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
+        if (__shfl(before, 0) != (int)gridDim.x - 1) return;
+        asm volatile("" ::: "memory");
+        v = 0.0;
+        for (int i = threadIdx.x; i < (int)gridDim.x; i += 64)
+            v += __hip_atomic_load(&w.sums[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    }
+    if (threadIdx.x == 0) {
+        const int32_t n = __hip_atomic_load(a.routed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        a.loss[0] = balance_loss(v, n, E, a.top_k);
     }
 }
 
@@ -477,10 +539,14 @@ __global__ __launch_bounds__(1024) void router_finish_kernel(const RouterArgs a)
 // One read of the logits and one write of the gradient; a token's lanes hold its row in registers
 // as in the forward pass.  What the chosen columns get extra is handed to the lanes that hold them
 // through LDS (a row of zeros per token, set, read by columns, and cleared again).
-template <class T, int kL, int kNC>
-__global__ __launch_bounds__(kThreads) void router_bwd_kernel(const RouterBwdArgs a)
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+template <class T, int kL, int kNC, bool kRenorm>
+__global__ __launch_bounds__(kThreads, 4) void router_bwd_kernel(const RouterBwdArgs a)
 {
     constexpr int kRows = 64 / kL, kCols = kL * kNC * 8;
+    constexpr bool kBf16 = __is_same(T, Bf16);
     constexpr int kSlots = (kRouterMaxTopK + kL - 1) / kL;   // entries of a token per lane
     __shared__ __attribute__((aligned(16))) float extra_lds[kWaves][kRows][kCols];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -491,32 +557,41 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(const RouterBwdArg
 #pragma unroll
         for (int j = 0; j < 8; ++j) extra[c + j] = 0.0f;
 
+    auto read_extra = [&](int i, float (&x)[8]) {
+        const float4* src = reinterpret_cast<const float4*>(extra + (i * kL + p) * 8);
+        const float4 lo = src[0], hi = src[1];
+        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+    };
+
     float g[kNC][8];
-    float f = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[i][j] = 0.0f;
     if (a.d_loss) {
         const float n = (float)max(a.routed[0], 1);
-        f = a.d_loss[0] * ((float)E / (float)k) / (n * n);
-    }
+        const float f = a.d_loss[0] * ((float)E / (float)k) / (n * n);
+        // (past the last column any count will do: p is zero there)
 #pragma unroll
-    for (int i = 0; i < kNC; ++i) {
-        const int c0 = chunk_start((i * kL + p) * 8, E);
+        for (int i = 0; i < kNC; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[i][j] = a.d_loss && c0 + j < E ? f * (float)a.counts[c0 + j] : 0.0f;
+            for (int j = 0; j < 8; ++j) g[i][j] = f * (float)a.counts[min((i * kL + p) * 8 + j, E - 1)];
     }
 
     const auto* logits = static_cast<const typename T::store_t*>(a.logits);
     const int64_t step = (int64_t)gridDim.x * kWaves * kRows;
     for (int64_t base = ((int64_t)blockIdx.x * kWaves + wave) * kRows; base < a.tokens; base += step) {
-        const int64_t t = base + slot;
-        const bool in = t < a.tokens;
+        const bool in = base + slot < a.tokens;
+        const int64_t t = in ? base + slot : a.tokens - 1;
         const auto* row = logits + t * a.ld;
-        const bool live = in && a.index[t * k] >= 0;
         Raw8<T> raw[kNC];
 #pragma unroll
-        for (int i = 0; i < kNC; ++i) raw[i] = load_logits<T>(row, (i * kL + p) * 8, E, live);
-        const float lse = live ? a.lse[t] : 0.0f;
+        for (int i = 0; i < kNC; ++i) raw[i] = load_logits<T, kL * kNC == 1>(row, (i * kL + p) * 8, E);
+        const bool live = in && a.index[t * k] >= 0;
+        const float lse = a.lse[t];
 
-        // the chosen columns: entry j0 + p of the token is this lane's
+        // the chosen columns: entries p, p + kL, ... of the token are this lane's
         int pos[kSlots];
         float dw[kSlots], w[kSlots];
 #pragma unroll
@@ -527,17 +602,17 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(const RouterBwdArg
             dw[q] = w[q] = 0.0f;
             if (live && j < k) idx = a.index[t * k + j];
             if (idx >= 0 && idx < E) {
-                pos[q] = (idx & ~7) + idx - chunk_start(idx & ~7, E);
+                pos[q] = idx;
                 if (a.d_weight) dw[q] = a.d_weight[t * k + j];
-                if (a.renorm) {
+                if constexpr (kRenorm) {
                     float v;
-                    if constexpr (sizeof(row[0]) == 2) v = as_float((uint32_t)row[idx] << 16);
+                    if constexpr (kBf16) v = as_float((uint32_t)row[idx] << 16);
                     else v = row[idx];
                     w[q] = expf(v - lse);
                 }
             }
         }
-        if (a.renorm) {
+        if constexpr (kRenorm) {
             float sw = 0.0f, sd = 0.0f;
 #pragma unroll
             for (int q = 0; q < kSlots; ++q) sw += w[q];
@@ -558,51 +633,46 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(const RouterBwdArg
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 
-        float x[kNC][8], pr[kNC][8];
+        float pr[kNC][8];
         float dot = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNC; ++i) {
-            const float* src = extra + (i * kL + p) * 8;
-            float v[8];
+            float v[8], x[8];
+            read_extra(i, x);
             unpack8(raw[i], v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                x[i][j] = src[j];
-                pr[i][j] = expf(v[j] - lse);
+                pr[i][j] = kBf16 ? exp_fast(v[j] - lse) : exp_exact(v[j] - lse);
                 sum += pr[i][j];
-                dot += pr[i][j] * (a.renorm ? g[i][j] : g[i][j] + x[i][j]);
+                dot += pr[i][j] * (kRenorm ? g[i][j] : g[i][j] + x[j]);
             }
         }
         // (the sum is 1 but for lse's rounding, which matters where lse is large beside the log in it)
-        const float inv = 1.0f / sum_lanes<kL>(sum);
+        sum = sum_lanes<kL>(sum);
+        const float inv = lse == lse ? 1.0f / sum : lse;
         dot = sum_lanes<kL>(dot) * inv;
+
+        auto* out = static_cast<typename T::store_t*>(a.d_logits) + t * a.ld_d;
+#pragma unroll
+        for (int i = 0; i < kNC; ++i) {
+            const int col = (i * kL + p) * 8;
+            float d[8], x[8];
+            read_extra(i, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float pj = pr[i][j] * inv;
+                d[j] = kRenorm ? pj * (g[i][j] - dot) + x[j] : pj * (g[i][j] + x[j] - dot);
+            }
+            if (!in || col >= E) continue;
+            const Raw8<T> r = live ? pack8(T{}, d) : zero8<T>();
+            if (col + 8 <= E) store8(out + col, r);
+            else store_few(out + col, r, E - col);
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int q = 0; q < kSlots; ++q)
             if (pos[q] >= 0) extra[pos[q]] = 0.0f;
-
-        auto* out = static_cast<typename T::store_t*>(a.d_logits) + t * a.ld_d;
-#pragma unroll
-        for (int i = 0; i < kNC; ++i) {
-            const int col = (i * kL + p) * 8, c0 = chunk_start(col, E);
-            float d[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float pj = pr[i][j] * inv;
-                d[j] = a.renorm ? pj * (g[i][j] - dot) + x[i][j] : pj * (g[i][j] + x[i][j] - dot);
-                if (!live) d[j] = 0.0f;
-            }
-            if (!in || col >= E) continue;
-            const Raw8<T> r = pack8(T{}, d);
-            if (col == c0 && c0 + 8 <= E) {
-                store8(out + c0, r);
-            } else {   // the columns before `col` are the neighbour's
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c0 + j >= col && c0 + j < E) store_one(out + c0 + j, r, j);
-            }
-        }
     }
 }
 
@@ -625,13 +695,13 @@ hipError_t fwd_run(const RouterArgs& a, hipStream_t stream)
 {
     const dim3 grid((unsigned)a.blocks);
     if (a.counts) {
-        const size_t lds = (size_t)a.experts * 4 * (1 + kWaves);
-        router_fwd_kernel<T, kL, kNC, kK, true><<<grid, kThreads, lds, stream>>>(a);
+        const size_t lds = (size_t)a.experts * 4 * (1 + kFwdWaves);
+        router_fwd_kernel<T, kL, kNC, kK, true><<<grid, kFwdThreads, lds, stream>>>(a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || !a.workspace) return e;
         router_finish_kernel<<<(unsigned)finish_blocks(a.experts), 1024, 0, stream>>>(a);
     } else {
-        router_fwd_kernel<T, kL, kNC, kK, false><<<grid, kThreads, 0, stream>>>(a);
+        router_fwd_kernel<T, kL, kNC, kK, false><<<grid, kFwdThreads, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
@@ -651,8 +721,9 @@ template <class T, int kL, int kNC>
 hipError_t bwd_run(const RouterBwdArgs& a, hipStream_t stream)
 {
     const int64_t per = kWaves * (64 / kL);
-    const int64_t blocks = std::min<int64_t>((a.tokens + per - 1) / per, 2048);
-    router_bwd_kernel<T, kL, kNC><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    const int64_t blocks = std::min<int64_t>((a.tokens + per - 1) / per, 4 * device_cus());
+    if (a.renorm) router_bwd_kernel<T, kL, kNC, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    else router_bwd_kernel<T, kL, kNC, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -674,13 +745,13 @@ template <class T> hipError_t bwd_shape(const RouterBwdArgs& a, hipStream_t stre
 }  // namespace
 
 // Workgroups: one where it takes the tokens in at most four steps and the counts are asked for (no
-// second kernel then), else up to 1024 of them.
+// second kernel then), else up to 512 of them.
 int64_t router_fwd_blocks(int64_t tokens, int64_t experts, bool loss)
 {
-    const int64_t per = kWaves * (64 / shape_of(experts).lanes);
+    const int64_t per = kFwdWaves * (64 / shape_of(experts).lanes);
     const int64_t blocks = (tokens + per - 1) / per;
     if (loss && blocks <= 4) return 1;
-    return std::min<int64_t>(blocks, loss ? 1024 : 4096);
+    return std::min<int64_t>(blocks, loss ? 512 : 4096);
 }
 
 int64_t router_fwd_workspace_bytes(int64_t tokens, int64_t experts)

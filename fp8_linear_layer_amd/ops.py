@@ -10,6 +10,7 @@ its type, shape and strides) is checked here before its pointer is passed on.  A
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple
 
 import torch
@@ -51,47 +52,62 @@ def _refuse(message: str):
     raise _te.TeFp8Error(1, message)
 
 
+# (PyTorch's handle of the stream without the Stream object around it, whose making costs as much as a launch)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _tensor(t, name, dtypes, shape, device, contiguous=True):
-    """Refuse a tensor that is not on `device`, of one of the dtypes and of the shape (with
-    contiguous=False: rows of consecutive elements at any stride)."""
-    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_cuda:
+def _tensor(t, name, dtype, shape, device):
+    """Refuse a tensor that is not a contiguous one of the type and shape on the device."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        _refuse(f"{name}: expected a tensor on {device}")
+    if t.dtype is not dtype:
+        _refuse(f"{name}: expected {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        _refuse(f"{name}: expected shape {shape} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        _refuse(f"{name}: expected a contiguous tensor")
+
+
+def _rows(t, name, dtypes, shape, device):
+    """The same for a matrix whose rows may lie at any stride; returns the stride."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
         _refuse(f"{name}: expected a tensor on {device}")
     if t.dtype not in dtypes:
-        _refuse(f"{name}: expected {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
-        _refuse(f"{name}: expected shape {tuple(shape)} (got {tuple(t.shape)})")
-    if contiguous:
-        if not t.is_contiguous():
-            _refuse(f"{name}: expected a contiguous tensor")
-    elif t.numel() and ((shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1])):
-        _refuse(f"{name}: expected rows of consecutive elements that do not overlap (strides {t.stride()})")
-
-
-def _ld(t):
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else _row_ld(t)
-
-
-def _row_ld(t):
-    # (the stride of a single row is of no meaning; fp8 rows want a multiple of 16)
-    n = t.shape[1]
-    return (n + 15) // 16 * 16
+        _refuse(f"{name}: expected {' or '.join(map(str, dtypes))} (got {t.dtype})")
+    if t.shape != shape:
+        _refuse(f"{name}: expected shape {shape} (got {tuple(t.shape)})")
+    return _ld(t, name)
 
 
 def _matrix(t, name):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
+    """Refuse what is no bf16 or fp32 matrix on the GPU with rows of consecutive elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         _refuse(f"{name}: expected a matrix on the GPU")
     if t.dtype not in _TYPE:
         _refuse(f"{name}: expected torch.bfloat16 or torch.float32 (got {t.dtype})")
-    if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
+    return _ld(t, name)
+
+
+def _ld(t, name):
+    """The row stride.  (That of a single row is of no meaning; fp8 rows want a multiple of 16.)"""
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if t.numel() and ((cols > 1 and one != 1) or (rows > 1 and ld < cols)):
         _refuse(f"{name}: expected rows of consecutive elements that do not overlap (strides {t.stride()})")
+    return ld if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _new(shape, dtype, device):
+    return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=device)
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
@@ -114,68 +130,73 @@ def te_rmsnorm_fwd(x, gamma, eps=1e-5, residual=None, out_dtype=_BF16, flags=0, 
     fp32 (y), or in fp8 as its per-token cast (q, scales; rowwise) and / or the cast of its transpose
     (qt, scales_t; transpose).  x and residual are bf16 or fp32 [rows, cols], gamma bf16 [cols].
     Outputs that are not given are allocated; h=residual adds in place."""
-    lib = _lib()
-    _matrix(x, "x")
-    rows, cols = x.shape
+    lib = _bound or _lib()
+    ld_x = _matrix(x, "x")
+    shape = rows, cols = x.shape
     device = x.device
-    _tensor(gamma, "gamma", (torch.bfloat16,), (cols,), device)
-    if out_dtype not in _TORCH:
-        _refuse(f"out_dtype: no type {out_dtype}")
-    fp8 = out_dtype not in (_BF16, _F32)
+    _tensor(gamma, "gamma", torch.bfloat16, (cols,), device)
+    ld_res = ld_h = ld_y = ld_qt = 0
     if residual is not None:
-        _tensor(residual, "residual", _FLOATS, (rows, cols), device, contiguous=False)
+        ld_res = _rows(residual, "residual", _FLOATS, shape, device)
         if h is None:
-            h = torch.empty((rows, cols), dtype=residual.dtype, device=device)
+            h, ld_h = _new(shape, residual.dtype, device), cols
         else:
-            _tensor(h, "h", (residual.dtype,), (rows, cols), device, contiguous=False)
+            ld_h = _rows(h, "h", (residual.dtype,), shape, device)
     elif h is not None:
         _refuse("h: given without a residual")
     if rstd is None:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=device)
+        rstd = _new((rows,), torch.float32, device)
     else:
-        _tensor(rstd, "rstd", (torch.float32,), (rows,), device)
-    if not fp8:
+        _tensor(rstd, "rstd", torch.float32, (rows,), device)
+    main = None
+    if out_dtype == _BF16 or out_dtype == _F32:
         if transpose or q is not None or scales is not None or qt is not None or scales_t is not None:
             _refuse("transpose, q, scales, qt and scales_t belong to fp8 outputs")
         if y is None:
-            y = torch.empty((rows, cols), dtype=_TORCH[out_dtype], device=device)
+            y, ld_y = _new(shape, _TORCH[out_dtype], device), cols
         else:
-            _tensor(y, "y", (_TORCH[out_dtype],), (rows, cols), device, contiguous=False)
+            ld_y = _rows(y, "y", (_TORCH[out_dtype],), shape, device)
         main = y
     else:
+        if out_dtype not in _TORCH:
+            _refuse(f"out_dtype: no type {out_dtype}")
         if y is not None:
             _refuse("y: fp8 outputs are q and scales")
-        if (not rowwise and (q is not None or scales is not None)) or \
-                (not transpose and (qt is not None or scales_t is not None)):
-            _refuse("an fp8 output was given that the call does not write")
         if rowwise:
             if cols % 128:
                 _refuse(f"cols must be a multiple of 128 for the fp8 cast (got {cols})")
             if q is None:
-                q = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+                q, ld_y = _new(shape, torch.uint8, device), cols
             else:
-                _tensor(q, "q", (torch.uint8,), (rows, cols), device, contiguous=False)
+                ld_y = _rows(q, "q", (torch.uint8,), shape, device)
+            main = q
+            s_shape = (cols // 128, (rows + 3) // 4 * 4)
             if scales is None:
-                scales = torch.empty((cols // 128, (rows + 3) // 4 * 4), dtype=torch.float32, device=device)
+                scales = _new(s_shape, torch.float32, device)
             else:
-                _tensor(scales, "scales", (torch.float32,), (cols // 128, (rows + 3) // 4 * 4), device)
+                _tensor(scales, "scales", torch.float32, s_shape, device)
+        elif q is not None or scales is not None:
+            _refuse("q and scales: given with rowwise=False")
         if transpose:
             if rows % 128 or cols % 8:
                 _refuse(f"rows must be a multiple of 128 and cols of 8 for the cast of the transpose (got {rows}, {cols})")
             if qt is None:
-                qt = torch.empty((cols, rows), dtype=torch.uint8, device=device)
+                qt, ld_qt = _new((cols, rows), torch.uint8, device), rows
             else:
-                _tensor(qt, "qt", (torch.uint8,), (cols, rows), device, contiguous=False)
+                ld_qt = _rows(qt, "qt", (torch.uint8,), (cols, rows), device)
+            t_shape = (rows // 128, (cols + 3) // 4 * 4)
             if scales_t is None:
-                scales_t = torch.empty((rows // 128, (cols + 3) // 4 * 4), dtype=torch.float32, device=device)
+                scales_t = _new(t_shape, torch.float32, device)
             else:
-                _tensor(scales_t, "scales_t", (torch.float32,), (rows // 128, (cols + 3) // 4 * 4), device)
-        main = q
-    _te._check(lib.te_rmsnorm_fwd(
-        x.data_ptr(), _TYPE[x.dtype], _ld(x), _ptr(residual), _TYPE[residual.dtype] if residual is not None else 0,
-        _ld(residual) if residual is not None else 0, gamma.data_ptr(), eps, rows, cols, _ptr(h),
-        _ld(h) if h is not None else 0, rstd.data_ptr(), _ptr(main), out_dtype, _ld(main) if main is not None else 0,
-        flags, _ptr(scales), _ptr(qt), _ld(qt) if qt is not None else 0, _ptr(scales_t), _stream(stream, device)))
+                _tensor(scales_t, "scales_t", torch.float32, t_shape, device)
+        elif qt is not None or scales_t is not None:
+            _refuse("qt and scales_t: given with transpose=False")
+    status = lib.te_rmsnorm_fwd(
+        x.data_ptr(), _TYPE[x.dtype], ld_x, _ptr(residual), 0 if residual is None else _TYPE[residual.dtype], ld_res,
+        gamma.data_ptr(), eps, rows, cols, _ptr(h), ld_h, rstd.data_ptr(), _ptr(main), out_dtype, ld_y, flags, _ptr(scales),
+        _ptr(qt), ld_qt, _ptr(scales_t), _stream(stream, device))
+    if status:
+        _te._check(status)
     return RmsNormOutput(h, rstd, y, q, scales, qt, scales_t)
 
 
@@ -183,32 +204,33 @@ def te_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dh=None, dgamma=None, need_dga
     """The norm's gradient: (dh, dgamma) for dy [rows, cols] (bf16 or fp32) and what the norm was of,
     h (x without a residual).  dres (h's type) is added to dh; dh=dres adds in place.  dgamma is
     fp32 [cols], None with need_dgamma=False.  The workspace (bytes) is allocated when not given."""
-    lib = _lib()
-    _matrix(h, "h")
-    rows, cols = h.shape
+    lib = _bound or _lib()
+    ld_h = _matrix(h, "h")
+    shape = rows, cols = h.shape
     device = h.device
-    _tensor(dy, "dy", _FLOATS, (rows, cols), device, contiguous=False)
-    _tensor(rstd, "rstd", (torch.float32,), (rows,), device)
-    _tensor(gamma, "gamma", (torch.bfloat16,), (cols,), device)
-    if dres is not None:
-        _tensor(dres, "dres", (h.dtype,), (rows, cols), device, contiguous=False)
+    ld_dy = _rows(dy, "dy", _FLOATS, shape, device)
+    _tensor(rstd, "rstd", torch.float32, (rows,), device)
+    _tensor(gamma, "gamma", torch.bfloat16, (cols,), device)
+    ld_res = 0 if dres is None else _rows(dres, "dres", (h.dtype,), shape, device)
     if dh is None:
-        dh = torch.empty((rows, cols), dtype=h.dtype, device=device)
+        dh, ld_dh = _new(shape, h.dtype, device), cols
     else:
-        _tensor(dh, "dh", (h.dtype,), (rows, cols), device, contiguous=False)
+        ld_dh = _rows(dh, "dh", (h.dtype,), shape, device)
     if not need_dgamma:
         if dgamma is not None:
             _refuse("dgamma: given with need_dgamma=False")
     else:
         if dgamma is None:
-            dgamma = torch.empty((cols,), dtype=torch.float32, device=device)
+            dgamma = _new((cols,), torch.float32, device)
         else:
-            _tensor(dgamma, "dgamma", (torch.float32,), (cols,), device)
+            _tensor(dgamma, "dgamma", torch.float32, (cols,), device)
         workspace = _workspace(workspace, lib.te_rmsnorm_bwd_workspace_bytes(rows, cols), device)
-    _te._check(lib.te_rmsnorm_bwd(
-        dy.data_ptr(), _TYPE[dy.dtype], _ld(dy), h.data_ptr(), _TYPE[h.dtype], _ld(h), rstd.data_ptr(),
-        gamma.data_ptr(), rows, cols, _ptr(dres), _ld(dres) if dres is not None else 0, dh.data_ptr(), _ld(dh),
-        _ptr(dgamma), _ptr(workspace), _nbytes(workspace), _stream(stream, device)))
+    status = lib.te_rmsnorm_bwd(
+        dy.data_ptr(), _TYPE[dy.dtype], ld_dy, h.data_ptr(), _TYPE[h.dtype], ld_h, rstd.data_ptr(), gamma.data_ptr(), rows,
+        cols, _ptr(dres), ld_res, dh.data_ptr(), ld_dh, _ptr(dgamma), _ptr(workspace), _nbytes(workspace),
+        _stream(stream, device))
+    if status:
+        _te._check(status)
     return dh, dgamma
 
 
@@ -218,8 +240,8 @@ def _nbytes(t):
 
 def _workspace(given, need, device):
     if given is None:
-        return torch.empty((need,), dtype=torch.uint8, device=device) if need else None
-    if not given.is_cuda or given.device != device or not given.is_contiguous():
+        return _new((need,), torch.uint8, device) if need else None
+    if given.device != device or not given.is_contiguous():
         _refuse(f"workspace: expected a contiguous tensor on {device}")
     return given
 
@@ -240,27 +262,31 @@ def te_moe_router_fwd(logits, top_k, renormalize=False, token_mask=None, loss=Fa
     logits are bf16 or fp32 [tokens, experts], -inf closes an expert, token_mask (bool or uint8
     [tokens]) leaves tokens out.  With loss also the tokens per expert, the number of routed tokens
     and the balance loss.  lse, which the backward pass needs, comes with loss or need_lse."""
-    lib = _lib()
-    _matrix(logits, "logits")
+    lib = _bound or _lib()
+    ld = _matrix(logits, "logits")
     tokens, experts = logits.shape
     device = logits.device
     if not 1 <= top_k <= max(experts, 1):
         _refuse(f"top_k must be in [1, experts] (got {top_k} of {experts})")
-    if token_mask is not None:
-        _tensor(token_mask, "token_mask", (torch.bool, torch.uint8), (tokens,), device)
-    index = torch.empty((tokens, top_k), dtype=torch.int32, device=device)
-    weight = torch.empty((tokens, top_k), dtype=torch.float32, device=device)
-    lse = torch.empty((tokens,), dtype=torch.float32, device=device) if (loss if need_lse is None else need_lse) else None
+    if token_mask is not None and token_mask.dtype is not torch.uint8:
+        _tensor(token_mask, "token_mask", torch.bool, (tokens,), device)
+    elif token_mask is not None:
+        _tensor(token_mask, "token_mask", torch.uint8, (tokens,), device)
+    index = _new((tokens, top_k), torch.int32, device)
+    weight = _new((tokens, top_k), torch.float32, device)
+    lse = _new((tokens,), torch.float32, device) if (loss if need_lse is None else need_lse) else None
     counts = routed = out = None
     if loss:
-        counts = torch.empty((experts,), dtype=torch.int32, device=device)
-        routed = torch.empty((1,), dtype=torch.int32, device=device)
-        out = torch.empty((1,), dtype=torch.float32, device=device)
+        counts = _new((experts,), torch.int32, device)
+        routed = _new((1,), torch.int32, device)
+        out = _new((1,), torch.float32, device)
         workspace = _workspace(workspace, lib.te_moe_router_workspace_bytes(tokens, experts), device)
-    _te._check(lib.te_moe_router_fwd(
-        logits.data_ptr(), _TYPE[logits.dtype], _ld(logits), tokens, experts, top_k, bool(renormalize),
-        _ptr(token_mask), index.data_ptr(), weight.data_ptr(), _ptr(lse), _ptr(counts), _ptr(routed), _ptr(out),
-        _ptr(workspace), _nbytes(workspace), _stream(stream, device)))
+    status = lib.te_moe_router_fwd(
+        logits.data_ptr(), _TYPE[logits.dtype], ld, tokens, experts, top_k, bool(renormalize), _ptr(token_mask),
+        index.data_ptr(), weight.data_ptr(), _ptr(lse), _ptr(counts), _ptr(routed), _ptr(out), _ptr(workspace),
+        _nbytes(workspace), _stream(stream, device))
+    if status:
+        _te._check(status)
     return RouterOutput(index, weight, lse, counts, routed, out)
 
 
@@ -268,36 +294,42 @@ def te_moe_router_bwd(logits, index, lse, counts=None, routed=None, d_weight=Non
                       d_logits=None, stream=None):
     """d_logits [tokens, experts] for the gradients of the weights (d_weight, fp32 [tokens, top_k]) and
     of the balance loss (d_loss, fp32 [1] on the GPU, with the forward call's counts and routed)."""
-    lib = _lib()
-    _matrix(logits, "logits")
-    tokens, experts = logits.shape
+    lib = _bound or _lib()
+    ld = _matrix(logits, "logits")
+    shape = tokens, experts = logits.shape
     device = logits.device
     if not isinstance(index, torch.Tensor) or index.dim() != 2:
         _refuse("index: expected a matrix")
     top_k = index.shape[1]
-    _tensor(index, "index", (torch.int32,), (tokens, top_k), device)
-    _tensor(lse, "lse", (torch.float32,), (tokens,), device)
+    _tensor(index, "index", torch.int32, (tokens, top_k), device)
+    _tensor(lse, "lse", torch.float32, (tokens,), device)
     if d_weight is not None:
-        _tensor(d_weight, "d_weight", (torch.float32,), (tokens, top_k), device)
+        _tensor(d_weight, "d_weight", torch.float32, (tokens, top_k), device)
     if d_loss is not None:
         if not isinstance(d_loss, torch.Tensor) or d_loss.numel() != 1:
             _refuse("d_loss: expected one number")
-        _tensor(d_loss, "d_loss", (torch.float32,), d_loss.shape, device)
-        _tensor(counts, "counts", (torch.int32,), (experts,), device)
-        _tensor(routed, "routed", (torch.int32,), (1,), device)
-    if d_logits is None:
-        d_logits = torch.empty((tokens, experts), dtype=logits.dtype, device=device)
+        _tensor(d_loss, "d_loss", torch.float32, d_loss.shape, device)
+        _tensor(counts, "counts", torch.int32, (experts,), device)
+        _tensor(routed, "routed", torch.int32, (1,), device)
     else:
-        _tensor(d_logits, "d_logits", (logits.dtype,), (tokens, experts), device, contiguous=False)
-    _te._check(lib.te_moe_router_bwd(
-        logits.data_ptr(), _TYPE[logits.dtype], _ld(logits), tokens, experts, top_k, bool(renormalize),
-        index.data_ptr(), lse.data_ptr(), _ptr(d_weight), _ptr(counts) if d_loss is not None else None,
-        _ptr(routed) if d_loss is not None else None, _ptr(d_loss), d_logits.data_ptr(), _ld(d_logits),
-        _stream(stream, device)))
+        counts = routed = None
+    if d_logits is None:
+        d_logits, ld_d = _new(shape, logits.dtype, device), experts
+    else:
+        ld_d = _rows(d_logits, "d_logits", (logits.dtype,), shape, device)
+    status = lib.te_moe_router_bwd(
+        logits.data_ptr(), _TYPE[logits.dtype], ld, tokens, experts, top_k, bool(renormalize), index.data_ptr(),
+        lse.data_ptr(), _ptr(d_weight), _ptr(counts), _ptr(routed), _ptr(d_loss), d_logits.data_ptr(), ld_d,
+        _stream(stream, device))
+    if status:
+        _te._check(status)
     return d_logits
 
 
-class _GradTensor(ctypes.Structure):
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+
+
+class _GradTensor(ctypes.Structure):     # te_grad_tensor_t: four 64-bit words
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
                 ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
@@ -307,31 +339,44 @@ def te_grad_norm_clip(grads, max_norm, out=None, norm=None, workspace=None, stre
     min(1, max_norm / (norm + 1e-6)).  Gradients and outputs are lists of dense bf16 or fp32 tensors,
     each with a type of its own; without out the gradients are clipped in place.  Nothing is copied
     to the host."""
-    lib = _lib()
+    lib = _bound or _lib()
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        _refuse(f"out: {len(outs)} tensors for {len(grads)} gradients")
-    device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device()) if norm is None else norm.device
-    arr = (_GradTensor * len(grads))()
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        kind, okind = _TYPE.get(g.dtype), _TYPE.get(o.dtype)
-        if not g.is_cuda or g.device != device or o.device != device:
-            _refuse(f"gradient {i}: expected gradient and output on {device if device.type == 'cuda' else 'the GPU'}")
-        if kind is None or okind is None:
-            _refuse(f"gradient {i}: expected torch.bfloat16 or torch.float32 (got {g.dtype}, {o.dtype})")
-        if o is not g and o.shape != g.shape:
-            _refuse(f"gradient {i}: output of shape {tuple(o.shape)} for {tuple(g.shape)}")
-        if not (g.is_contiguous() and (o is g or o.is_contiguous())) and not _same_dense(g, o):
-            _refuse(f"gradient {i}: expected dense tensors of one layout")
-        arr[i] = (g.data_ptr(), o.data_ptr(), g.numel(), kind, okind)
-    if norm is None:
-        norm = torch.empty((1,), dtype=torch.float32, device=device)
+    n = len(grads)
+    if len(outs) != n:
+        _refuse(f"out: {len(outs)} tensors for {n} gradients")
+    if n:
+        device = grads[0].device
     else:
-        _tensor(norm, "norm", (torch.float32,), (1,), device)
-    workspace = _workspace(workspace, lib.te_grad_norm_workspace_bytes(len(grads)), device)
-    _te._check(lib.te_grad_norm_clip(arr, len(grads), max_norm, norm.data_ptr(), _ptr(workspace), _nbytes(workspace),
-                                     _stream(stream, device)))
+        device = torch.device("cuda", torch.cuda.current_device()) if norm is None else norm.device
+    # (lists of one property at a time: training steps pass hundreds of tensors, and this is a third of
+    # the time that a loop over them with all the checks in it takes)
+    if not all([t.is_cuda for t in grads]) or len({t.device for t in grads} | {t.device for t in outs}) > 1:
+        _refuse("expected gradients and outputs on one GPU")
+    types = [_TYPE.get(t.dtype) for t in grads]
+    out_types = types if outs is grads else [_TYPE.get(t.dtype) for t in outs]
+    if None in types or None in out_types:
+        _refuse(f"expected torch.bfloat16 or torch.float32 (got {({t.dtype for t in grads + outs})})")
+    if outs is not grads and [t.shape for t in grads] != [t.shape for t in outs]:
+        _refuse("out: expected the gradients' shapes")
+    if not (all([t.is_contiguous() for t in grads]) and (outs is grads or all([t.is_contiguous() for t in outs]))):
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if not (g.is_contiguous() and o.is_contiguous()) and not _same_dense(g, o):
+                _refuse(f"gradient {i}: expected dense tensors of one layout")
+    fields = [0] * (4 * n)
+    fields[0::4] = map(_data_ptr, grads)
+    fields[1::4] = map(_data_ptr, outs)
+    fields[2::4] = map(_numel, grads)
+    fields[3::4] = [g | o << 32 for g, o in zip(types, out_types)]
+    if norm is None:
+        norm = _new((1,), torch.float32, device)
+    else:
+        _tensor(norm, "norm", torch.float32, (1,), device)
+    workspace = _workspace(workspace, lib.te_grad_norm_workspace_bytes(n), device)
+    status = lib.te_grad_norm_clip(struct.pack(f"{4 * n}q", *fields), n, max_norm, norm.data_ptr(), _ptr(workspace),
+                                   _nbytes(workspace), _stream(stream, device))
+    if status:
+        _te._check(status)
     return norm
 
 
