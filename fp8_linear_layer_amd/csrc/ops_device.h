@@ -13,6 +13,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 // sixteen bytes take any address on this target, so rows of odd length or stride need no other path.
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t uint32_a2 __attribute__((aligned(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
