@@ -1,16 +1,19 @@
-"""Build libte_fp8.so (the gfx950 HIP kernels + the C ABI) in-tree with hipcc."""
+"""Build libte_fp8.so (the gfx950 HIP kernels + the C ABI) and _te_ops.so (the Python side of the
+operators around the GEMMs) in-tree."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libte_fp8.so")
+BINDING = os.path.join(PKG, "_te_ops.so")
 # (source, object, extra flags): gemm.hip is compiled once per operand-format pair and once for its
 # host side (TE_GEMM_PART), so its kernel instantiations build in parallel
 SOURCES = [("api.cpp", "api.o", []), ("api_ops.cpp", "api_ops.o", []), ("cast.hip", "cast.o", []),
@@ -43,10 +46,29 @@ def _compile(job, verbose: bool) -> str:
     return obj
 
 
+def _build_binding(verbose: bool) -> str:
+    """binding.cpp against PyTorch's headers and libraries (host code only)."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           *[f"-isystem{p}" for p in [*include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include"]],
+           os.path.join(CSRC, "binding.cpp"), *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_build_binding, verbose)
         objs = list(ex.map(lambda j: _compile(j, verbose), SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

@@ -181,8 +181,9 @@ def test_validation_under_sanitizers(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-fPIC", "-shared", *SAN, "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
                     "-I", os.path.join(ROOT, "include"), "-I", csrc, os.path.join(csrc, "api.cpp"), os.path.join(csrc, "api_ops.cpp"),
                     os.path.join(sub, "host_stubs.cpp"), os.path.join(sub, "host_stubs_ops.cpp"), "-o", out], check=True)
-    libasan = subprocess.check_output(["gcc", "-print-file-name=libasan.so"], text=True).strip()
-    env = dict(os.environ, LD_PRELOAD=libasan, TE_FP8_TEST_LIB=out, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1",
+    # (the C++ runtime beside the sanitizer's: the binding throws, and the sanitizer wants to know how before that)
+    preload = [subprocess.check_output(["gcc", f"-print-file-name={n}"], text=True).strip() for n in ("libasan.so", "libstdc++.so.6")]
+    env = dict(os.environ, LD_PRELOAD=" ".join(preload), TE_FP8_TEST_LIB=out, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1",
                UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider", "-m", "not gpu",
                         os.path.abspath(__file__)], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
