@@ -35,6 +35,7 @@ struct NormFwdArgs {
     int cols;
     float eps;
     bool x_bf16, h_bf16, src_bf16;
+    bool past;              // set by the launcher: read past the caches
     NormOut out;
     int fmt, pow2;
 };
