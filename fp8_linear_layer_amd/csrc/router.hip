@@ -213,16 +213,23 @@ __device__ __forceinline__ void merge_lanes(TopList<T, kK>& l)
     if constexpr (kL > 32) merge<32>(l);
 }
 
-// The eight logits from column `col` on; columns past the last read as -inf.  (The last chunk of a row
-// whose length is no multiple of eight is loaded from experts - 8 and moved to the front.)
-template <class T, bool kFew, class P>
-__device__ __forceinline__ Raw8<T> load_logits(const P* row, int col, int experts)
+// The lane's chunks of a row: the eight logits from each column (i kL + p) 8 on, columns past the last as
+// -inf.  (The last chunk of a row whose length is no multiple of eight is loaded from experts - 8 and
+// moved to the front.  All loads come first: one that is waited for by itself costs its whole latency.)
+template <class T, int kL, int kNC, class P>
+__device__ __forceinline__ void load_logits(Raw8<T> (&r)[kNC], const P* row, int p, int experts)
 {
-    if (kFew && experts < 8) return load_few(row, experts, kNegInf);
-    const int c0 = min(col, experts - 8);
-    Raw8<T> r = load8(row + c0);
-    if (col != c0) r = col < experts ? drop_front(r, col - c0, kNegInf) : fill8<T>(kNegInf);
-    return r;
+    if (kL * kNC == 1 && experts < 8) {
+        r[0] = load_few(row, experts, kNegInf);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) r[i] = load8(row + min((i * kL + p) * 8, experts - 8));
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+        const int col = (i * kL + p) * 8, behind = col - (experts - 8);
+        if (behind > 0) r[i] = behind < 8 ? drop_front(r[i], behind, kNegInf) : fill8<T>(kNegInf);
+    }
 }
 
 // The workspace: a row per workgroup of counts (and, behind them, of its routed tokens) and of
@@ -311,8 +318,7 @@ __global__ __launch_bounds__(kFwdThreads, (kFwdWavesPerSimd<T, kNC, kK>)) void r
         const int64_t t = min(b + slot, a.tokens - 1);
         const auto* row = logits + t * a.ld;
         if (a.mask) m = a.mask[t];
-#pragma unroll
-        for (int i = 0; i < kNC; ++i) r[i] = load_logits<T, kL * kNC == 1>(row, (i * kL + p) * 8, E);
+        load_logits<T, kL>(r, row, p, E);
     };
     if (kAhead && base < a.tokens) fetch(base, next, next_unmasked);
     for (; base < a.tokens; base += step) {
@@ -585,29 +591,33 @@ __global__ __launch_bounds__(kThreads, 4) void router_bwd_kernel(const RouterBwd
         const bool in = base + slot < a.tokens;
         const int64_t t = in ? base + slot : a.tokens - 1;
         const auto* row = logits + t * a.ld;
-        Raw8<T> raw[kNC];
-#pragma unroll
-        for (int i = 0; i < kNC; ++i) raw[i] = load_logits<T, kL * kNC == 1>(row, (i * kL + p) * 8, E);
-        const bool live = in && a.index[t * k] >= 0;
-        const float lse = a.lse[t];
-
-        // the chosen columns: entries p, p + kL, ... of the token are this lane's
+        // The chosen columns: entries p, p + kL, ... of the token are this lane's.  (Everything that is
+        // read by the token is asked for here, before any of it is used.)
         int pos[kSlots];
         float dw[kSlots], w[kSlots];
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) {
-            const int j = q * kL + p;
-            int idx = -1;
             pos[q] = -1;
             dw[q] = w[q] = 0.0f;
-            if (live && j < k) idx = a.index[t * k + j];
-            if (idx >= 0 && idx < E) {
-                pos[q] = idx;
-                if (a.d_weight) dw[q] = a.d_weight[t * k + j];
-                if constexpr (kRenorm) {
+            if (q * kL >= k) continue;
+            const int64_t at = t * k + min(q * kL + p, k - 1);
+            pos[q] = a.index[at];
+            if (a.d_weight) dw[q] = a.d_weight[at];
+        }
+        const int first = a.index[t * k];
+        const float lse = a.lse[t];
+        Raw8<T> raw[kNC];
+        load_logits<T, kL>(raw, row, p, E);
+        const bool live = in && first >= 0;
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+            if (!live || q * kL + p >= k || pos[q] >= E) pos[q] = -1;
+            if (pos[q] < 0) dw[q] = 0.0f;
+            if constexpr (kRenorm) {
+                if (pos[q] >= 0) {
                     float v;
-                    if constexpr (kBf16) v = as_float((uint32_t)row[idx] << 16);
-                    else v = row[idx];
+                    if constexpr (kBf16) v = as_float((uint32_t)row[pos[q]] << 16);
+                    else v = row[pos[q]];
                     w[q] = expf(v - lse);
                 }
             }
