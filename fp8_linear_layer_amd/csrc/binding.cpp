@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -211,11 +212,14 @@ T* ptr(const at::Tensor& t)
 }
 int64_t bytes(const at::Tensor& t) { return t.defined() ? (int64_t)t.nbytes() : 0; }
 
-hipStream_t stream_of(PyObject* o, const at::Device& device)
+// The device's current stream: outputs and workspaces are allocated for it, so work on another one would
+// race with its earlier users of that memory.
+hipStream_t stream_of(const at::Device& device)
 {
-    PyObject* index = o == Py_None ? PyLong_FromLong(device.index()) : nullptr;
-    PyObject* handle = index ? PyObject_CallOneArg(current_stream, index) : PyObject_GetAttrString(o, "cuda_stream");
-    Py_XDECREF(index);
+    PyObject* index = PyLong_FromLong(device.index());
+    if (!index) throw PythonError();
+    PyObject* handle = PyObject_CallOneArg(current_stream, index);
+    Py_DECREF(index);
     if (!handle) throw PythonError();
     void* p = PyLong_AsVoidPtr(handle);
     Py_DECREF(handle);
@@ -249,11 +253,11 @@ void arguments(Py_ssize_t have, Py_ssize_t want)
     if (have != want) refuse("expected %zd arguments (got %zd)", want, have);
 }
 
-// (x, gamma, eps, residual, out_dtype, flags, rowwise, transpose, h, rstd, y, q, scales, qt, scales_t, stream)
+// (x, gamma, eps, residual, out_dtype, flags, rowwise, transpose, h, rstd, y, q, scales, qt, scales_t)
 PyObject* rmsnorm_fwd(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
     return guarded([&] {
-        arguments(n, 16);
+        arguments(n, 15);
         const at::Tensor x = required(v[0], "x"), gamma = required(v[1], "gamma"), residual = optional(v[3], "residual");
         const double eps = number(v[2]);
         const int64_t out = integer(v[4]), flags = integer(v[5]);
@@ -264,6 +268,7 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         const int64_t rows = x.size(0), cols = x.size(1);
         const int64_t shape[2] = {rows, cols};
         const at::Device device = x.device();
+        const c10::DeviceGuard guard(device);
         array(gamma, "gamma", kBf16, {cols}, device);
         int64_t ld_res = 0, ld_h = 0, ld_y = 0, ld_qt = 0;
         if (residual.defined()) {
@@ -298,16 +303,16 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         check(lib.rmsnorm_fwd(ptr(x), type_of(x), ld_x, ptr(residual), residual.defined() ? type_of(residual) : TE_DTYPE_BF16, ld_res,
                               ptr(gamma), (float)eps, rows, cols, ptr(h), ld_h, ptr<float>(rstd), y.defined() ? ptr(y) : ptr(q),
                               (te_dtype_t)out, ld_y, (uint32_t)flags, ptr<float>(scales), ptr(qt), ld_qt, ptr<float>(scales_t),
-                              stream_of(v[15], device)));
+                              stream_of(device)));
         return tuple_of({h, rstd, y, q, scales, qt, scales_t});
     });
 }
 
-// (dy, h, rstd, gamma, dres, dh, dgamma, need_dgamma, workspace, stream)
+// (dy, h, rstd, gamma, dres, dh, dgamma, need_dgamma, workspace)
 PyObject* rmsnorm_bwd(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
     return guarded([&] {
-        arguments(n, 10);
+        arguments(n, 9);
         const at::Tensor dy = required(v[0], "dy"), h = required(v[1], "h"), rstd = required(v[2], "rstd"),
                          gamma = required(v[3], "gamma"), dres = optional(v[4], "dres");
         at::Tensor dh = optional(v[5], "dh"), dgamma = optional(v[6], "dgamma"), workspace = optional(v[8], "workspace");
@@ -316,6 +321,7 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         const int64_t rows = h.size(0), cols = h.size(1);
         const int64_t shape[2] = {rows, cols};
         const at::Device device = h.device();
+        const c10::DeviceGuard guard(device);
         const int64_t ld_dy = float_rows(dy, "dy", shape, device);
         array(rstd, "rstd", kF32, {rows}, device);
         array(gamma, "gamma", kBf16, {cols}, device);
@@ -329,16 +335,16 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         }
         check(lib.rmsnorm_bwd(ptr(dy), type_of(dy), ld_dy, ptr(h), type_of(h), ld_h, ptr<float>(rstd), ptr(gamma), rows, cols,
                               ptr(dres), ld_res, ptr(dh), ld_dh, ptr<float>(dgamma), ptr(workspace), bytes(workspace),
-                              stream_of(v[9], device)));
+                              stream_of(device)));
         return tuple_of({dh, dgamma});
     });
 }
 
-// (logits, top_k, renormalize, token_mask, loss, need_lse, workspace, stream)
+// (logits, top_k, renormalize, token_mask, loss, need_lse, workspace)
 PyObject* moe_router_fwd(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
     return guarded([&] {
-        arguments(n, 8);
+        arguments(n, 7);
         const at::Tensor logits = required(v[0], "logits"), mask = optional(v[3], "token_mask");
         const int64_t top_k = integer(v[1]);
         const bool renormalize = truth(v[2]), loss = truth(v[4]), need_lse = truth(v[5]);
@@ -346,6 +352,7 @@ PyObject* moe_router_fwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         const int64_t ld = matrix(logits, "logits");
         const int64_t tokens = logits.size(0), experts = logits.size(1);
         const at::Device device = logits.device();
+        const c10::DeviceGuard guard(device);
         if (top_k < 1 || top_k > experts)
             refuse("top_k must be in [1, experts] (got %lld of %lld)", (long long)top_k, (long long)experts);
         if (mask.defined()) array(mask, "token_mask", mask.scalar_type() == kU8 ? kU8 : at::kBool, {tokens}, device);
@@ -360,16 +367,16 @@ PyObject* moe_router_fwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         check(lib.moe_router_fwd(ptr(logits), type_of(logits), ld, tokens, experts, (int32_t)top_k, renormalize, ptr<uint8_t>(mask),
                                  ptr<int32_t>(index), ptr<float>(weight), ptr<float>(lse), ptr<int32_t>(counts),
                                  ptr<int32_t>(routed), ptr<float>(value), ptr(workspace), bytes(workspace),
-                                 stream_of(v[7], device)));
+                                 stream_of(device)));
         return tuple_of({index, weight, lse, counts, routed, value});
     });
 }
 
-// (logits, index, lse, counts, routed, d_weight, d_loss, renormalize, d_logits, stream)
+// (logits, index, lse, counts, routed, d_weight, d_loss, renormalize, d_logits)
 PyObject* moe_router_bwd(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
     return guarded([&] {
-        arguments(n, 10);
+        arguments(n, 9);
         const at::Tensor logits = required(v[0], "logits"), index = required(v[1], "index"), lse = required(v[2], "lse"),
                          d_weight = optional(v[5], "d_weight"), d_loss = optional(v[6], "d_loss");
         const bool renormalize = truth(v[7]);
@@ -377,6 +384,7 @@ PyObject* moe_router_bwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         const int64_t ld = matrix(logits, "logits");
         const int64_t tokens = logits.size(0), experts = logits.size(1);
         const at::Device device = logits.device();
+        const c10::DeviceGuard guard(device);
         if (index.dim() != 2) refuse("index: expected a matrix");
         const int64_t top_k = index.size(1);
         array(index, "index", kI32, {tokens, top_k}, device);
@@ -394,7 +402,7 @@ PyObject* moe_router_bwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         const int64_t ld_d = make_or_check_rows(d_logits, "d_logits", logits.scalar_type(), shape, device);
         check(lib.moe_router_bwd(ptr(logits), type_of(logits), ld, tokens, experts, (int32_t)std::min<int64_t>(top_k, INT32_MAX),
                                  renormalize, ptr<int32_t>(index), ptr<float>(lse), ptr<float>(d_weight), ptr<int32_t>(counts),
-                                 ptr<int32_t>(routed), ptr<float>(d_loss), ptr(d_logits), ld_d, stream_of(v[9], device)));
+                                 ptr<int32_t>(routed), ptr<float>(d_loss), ptr(d_logits), ld_d, stream_of(device)));
         return wrap(d_logits);
     });
 }
@@ -406,11 +414,11 @@ bool same_dense(const at::Tensor& g, const at::Tensor& o)
     return g.is_non_overlapping_and_dense() && o.is_non_overlapping_and_dense() && g.strides() == o.strides();
 }
 
-// (grads, max_norm, out, norm, workspace, stream): grads and out are lists or tuples, out may be None
+// (grads, max_norm, out, norm, workspace): grads and out are lists or tuples, out may be None
 PyObject* grad_norm_clip(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
     return guarded([&] {
-        arguments(n, 6);
+        arguments(n, 5);
         const double max_norm = number(v[1]);
         const bool in_place = v[2] == Py_None;
         if (!(PyList_Check(v[0]) || PyTuple_Check(v[0])) || !(in_place || PyList_Check(v[2]) || PyTuple_Check(v[2])))
@@ -434,10 +442,11 @@ PyObject* grad_norm_clip(PyObject*, PyObject* const* v, Py_ssize_t n)
             list[(size_t)i] = te_grad_tensor_t{g.data_ptr(), o.data_ptr(), g.numel(), type_of(g), type_of(o)};
         }
         if (!device.is_cuda()) refuse("norm: expected a tensor on the GPU");
+        const c10::DeviceGuard guard(device);
         make_or_check(norm, "norm", kF32, {1}, device);
         workspace_for(workspace, lib.grad_norm_workspace_bytes(count), device);
         check(lib.grad_norm_clip(list.data(), count, (float)max_norm, ptr<float>(norm), ptr(workspace), bytes(workspace),
-                                 stream_of(v[5], device)));
+                                 stream_of(device)));
         return wrap(norm);
     });
 }

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void rmsnorm_fwd_kernel(const Nor
     constexpr int kRows = kThreadsOf<kTPR> / kTPR;
     __shared__ float red[kThreadsOf<kTPR> / 64];
     // rows past the end repeat the last one and store nothing
-    const int64_t row_raw = xcd_run(blockIdx.x, gridDim.x) * kRows + threadIdx.x / kTPR;
+    const int64_t row_raw = a.first_row + xcd_run(blockIdx.x, gridDim.x) * kRows + threadIdx.x / kTPR;
     const bool in = row_raw < a.rows;
     const int64_t row = in ? row_raw : a.rows - 1;
     const int t = threadIdx.x % kTPR, cols = a.cols;
@@ -441,9 +441,15 @@ template <class X, class H, Out kOut> struct Fwd {
     template <int kTPR, int kNV> struct Rows {
         static void run(const NormFwdArgs& a, hipStream_t stream)
         {
-            constexpr int kRows = kThreadsOf<kTPR> / kTPR;
-            rmsnorm_fwd_kernel<X, H, kOut, kTPR, kNV>
-                <<<(unsigned)((a.rows + kRows - 1) / kRows), kThreadsOf<kTPR>, 0, stream>>>(a);
+            constexpr int kThreads = kThreadsOf<kTPR>, kRows = kThreads / kTPR;
+            // (a launch has at most 2^32 threads: more rows than that take several)
+            constexpr int64_t kMost = ((int64_t)1 << 31) / kThreads * kRows;
+            NormFwdArgs part = a;
+            for (part.first_row = 0; part.first_row < a.rows; part.first_row += kMost) {
+                const int64_t rows = std::min(kMost, a.rows - part.first_row);
+                rmsnorm_fwd_kernel<X, H, kOut, kTPR, kNV>
+                    <<<(unsigned)((rows + kRows - 1) / kRows), kThreads, 0, stream>>>(part);
+            }
         }
     };
 };
@@ -476,7 +482,6 @@ template <class S, int kFmt, bool kPow2>
 hipError_t transpose_run(const NormFwdArgs& a, hipStream_t stream)
 {
     const int64_t tiles = a.rows / kCT * ((a.cols + kCW - 1) / kCW);
-    if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
     rmsnorm_cast_transpose_kernel<S, kFmt, kPow2><<<(unsigned)tiles, kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -511,8 +516,8 @@ hipError_t launch_rmsnorm_fwd(const NormFwdArgs& args, hipStream_t stream)
 {
     NormFwdArgs a = args;
     if (a.rows <= 0) return hipSuccess;
-    if (a.rows > 0x7FFFFFFF) return hipErrorInvalidValue;
-    a.past = past_caches(a.rows * a.cols * ((a.x_bf16 ? 2 : 4) + (a.res ? a.h_bf16 ? 2 : 4 : 0)));
+    if (a.qt && a.rows / kCT * ((a.cols + kCW - 1) / kCW) >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidValue;
+    a.past = a.cols >= 8 && past_caches(a.rows * a.cols * ((a.x_bf16 ? 2 : 4) + (a.res ? a.h_bf16 ? 2 : 4 : 0)));
     hipError_t e = a.x_bf16 ? fwd_res<Bf16>(a, stream) : fwd_res<F32>(a, stream);
     if (e != hipSuccess || !a.qt) return e;
     return a.src_bf16 ? fwd_transpose<Bf16>(a, stream) : fwd_transpose<F32>(a, stream);

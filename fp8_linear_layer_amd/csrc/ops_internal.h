@@ -35,7 +35,9 @@ struct NormFwdArgs {
     int cols;
     float eps;
     bool x_bf16, h_bf16, src_bf16;
-    bool past;              // set by the launcher: read past the caches
+    // set by the launcher:
+    int64_t first_row;      // of this launch
+    bool past;              // read past the caches
     NormOut out;
     int fmt, pow2;
 };

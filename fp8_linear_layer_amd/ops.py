@@ -97,21 +97,30 @@ class RouterOutput(NamedTuple):
     loss: torch.Tensor | None     # fp32 [1]
 
 
+def _call(name, stream, *args):
+    """The native call on a given stream: made that stream the current one, so that what the call
+    allocates belongs to it too."""
+    if stream is None:
+        return getattr(_native or _load(), name)(*args)
+    with torch.cuda.stream(stream):
+        return getattr(_native or _load(), name)(*args)
+
+
 def te_rmsnorm_fwd(x, gamma, eps=1e-5, residual=None, out_dtype=_te.TE_DTYPE_BF16, flags=0, rowwise=True, transpose=False,
                    h=None, rstd=None, y=None, q=None, scales=None, qt=None, scales_t=None, stream=None) -> RmsNormOutput:
     """h = x + residual (in the residual's type), y = h / rms(h) * gamma, stored by out_dtype as bf16 /
     fp32 (y), or in fp8 as its per-token cast (q, scales; rowwise) and / or the cast of its transpose
     (qt, scales_t; transpose).  x and residual are bf16 or fp32 [rows, cols], gamma bf16 [cols].
     Outputs that are not given are allocated; h=residual adds in place."""
-    return RmsNormOutput._make((_native or _load()).rmsnorm_fwd(
-        x, gamma, eps, residual, out_dtype, flags, rowwise, transpose, h, rstd, y, q, scales, qt, scales_t, stream))
+    return RmsNormOutput._make(_call("rmsnorm_fwd", stream, x, gamma, eps, residual, out_dtype, flags, rowwise, transpose,
+                                     h, rstd, y, q, scales, qt, scales_t))
 
 
 def te_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dh=None, dgamma=None, need_dgamma=True, workspace=None, stream=None):
     """The norm's gradient: (dh, dgamma) for dy [rows, cols] (bf16 or fp32) and what the norm was of,
     h (x without a residual).  dres (h's type) is added to dh; dh=dres adds in place.  dgamma is
     fp32 [cols], None with need_dgamma=False.  The workspace (bytes) is allocated when not given."""
-    return (_native or _load()).rmsnorm_bwd(dy, h, rstd, gamma, dres, dh, dgamma, need_dgamma, workspace, stream)
+    return _call("rmsnorm_bwd", stream, dy, h, rstd, gamma, dres, dh, dgamma, need_dgamma, workspace)
 
 
 def te_moe_router_fwd(logits, top_k, renormalize=False, token_mask=None, loss=False, need_lse=None, workspace=None,
@@ -120,16 +129,15 @@ def te_moe_router_fwd(logits, top_k, renormalize=False, token_mask=None, loss=Fa
     logits are bf16 or fp32 [tokens, experts], -inf closes an expert, token_mask (bool or uint8
     [tokens]) leaves tokens out.  With loss also the tokens per expert, the number of routed tokens
     and the balance loss.  lse, which the backward pass needs, comes with loss or need_lse."""
-    return RouterOutput._make((_native or _load()).moe_router_fwd(
-        logits, top_k, renormalize, token_mask, loss, loss if need_lse is None else need_lse, workspace, stream))
+    return RouterOutput._make(_call("moe_router_fwd", stream, logits, top_k, renormalize, token_mask, loss,
+                                    loss if need_lse is None else need_lse, workspace))
 
 
 def te_moe_router_bwd(logits, index, lse, counts=None, routed=None, d_weight=None, d_loss=None, renormalize=False,
                       d_logits=None, stream=None):
     """d_logits [tokens, experts] for the gradients of the weights (d_weight, fp32 [tokens, top_k]) and
     of the balance loss (d_loss, fp32 [1] on the GPU, with the forward call's counts and routed)."""
-    return (_native or _load()).moe_router_bwd(logits, index, lse, counts, routed, d_weight, d_loss, renormalize, d_logits,
-                                               stream)
+    return _call("moe_router_bwd", stream, logits, index, lse, counts, routed, d_weight, d_loss, renormalize, d_logits)
 
 
 def te_grad_norm_clip(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
@@ -143,4 +151,4 @@ def te_grad_norm_clip(grads, max_norm, out=None, norm=None, workspace=None, stre
         out = list(out)
     if not grads and norm is None:
         norm = torch.empty((1,), dtype=torch.float32, device="cuda")
-    return (_native or _load()).grad_norm_clip(grads, max_norm, out, norm, workspace, stream)
+    return _call("grad_norm_clip", stream, grads, max_norm, out, norm, workspace)

@@ -138,6 +138,30 @@ def test_more_elements_than_31_bits():
     assert float(out[0]) == 1.5 and float(out[n - 1]) == 2.0 and float(out[1 << 31]) == 6.0 and int((out != 0).sum()) == 3
 
 
+@pytest.mark.parametrize("gt", ["f32", "bf16"])
+@pytest.mark.parametrize("ot", ["f32", "bf16"])
+def test_totals_larger_than_the_caches(gt, ot):
+    """16384 chunks and more go past the caches; tensors at odd offsets and of odd sizes."""
+    sizes = [100_000_003, 5, 35_000_001]
+    g = gen(8)
+    flat = (torch.randn(sum(sizes) + 1, generator=g, device="cuda") * 1e-3).to(DT[gt])
+    out = torch.full((sum(sizes) + 3,), 7.0, dtype=DT[ot], device="cuda")
+    grads, outs = list(flat[1:].split(sizes)), list(out[1:-2].split(sizes))
+    norm = te.te_grad_norm_clip(grads, 1.0, out=outs)
+    check(grads, 1.0, norm, outs)
+    assert out[0] == 7.0 and (out[-2:] == 7.0).all()
+
+
+def test_given_stream():
+    grads = tensors([50000, 3], torch.float32, 7)
+    outs = [torch.empty_like(g) for g in grads]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    norm = te.te_grad_norm_clip(grads, 1e-3, out=outs, stream=side)
+    side.synchronize()
+    check(grads, 1e-3, norm, outs)
+
+
 def test_other_stream_and_graph():
     grads = tensors([5000, 77, 20001], torch.float32, 6)
     outs = [torch.empty_like(g, dtype=torch.bfloat16) for g in grads]

@@ -306,6 +306,48 @@ def test_offsets_past_32_bits():
     assert torch.equal(da, db) and torch.equal(ga, gb)
 
 
+def test_more_rows_than_one_launch_holds():
+    """2^28 rows of one column at sixteen threads each pass the threads of a launch."""
+    rows = (1 << 28) + 77
+    x = torch.full((rows, 1), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[-1], x[(1 << 27) + 5] = 0.5, -4.0
+    gamma = torch.full((1,), 3.0, dtype=torch.bfloat16, device="cuda")
+    r = te.te_rmsnorm_fwd(x, gamma, 0.0)
+    assert float(r.rstd[-1]) == 2.0 and float(r.rstd[(1 << 27) + 5]) == 0.25 and int((r.rstd == 0.5).sum()) == rows - 2
+    assert float(r.y[(1 << 27) + 5]) == -3.0 and int((r.y == 3.0).sum()) == rows - 1
+
+
+@pytest.mark.parametrize("rows,cols,ld,xt,ht", [(40000, 2049, 2051, "bf16", ""), (20000, 1030, 1033, "f32", "bf16"), (17000, 4096, 4096, "bf16", "f32"),
+                                                (9 << 20, 9, 9, "bf16", "")])
+def test_inputs_larger_than_the_caches(rows, cols, ld, xt, ht):
+    """Read past the caches (128 MiB and more), at odd lengths and strides."""
+    g = gen(cols)
+    x = normal(g, (rows, cols), DT[xt], 0.7, ld=ld, shift=1)
+    res = normal(g, (rows, cols), DT[ht], 2.0, ld=ld, shift=3) if ht else None
+    gamma = normal(g, (1, cols), torch.bfloat16, 0.1, 1.0)[0]
+    r = te.te_rmsnorm_fwd(x, gamma, EPS, residual=res)
+    y = check_fwd(x, res, gamma, r)
+    close(r.y, y, HALF[torch.bfloat16] + 40 * U, what="y")
+
+
+def test_given_stream_owns_what_the_call_allocates():
+    x = normal(gen(1), (512, 1024), torch.bfloat16)
+    gamma = normal(gen(2), (1, 1024), torch.bfloat16, 0.1, 1.0)[0]
+    want = te.te_rmsnorm_fwd(x, gamma)
+    dwant = te.te_rmsnorm_bwd(x, x, want.rstd, gamma)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    before = torch.cuda.current_stream()
+    for _ in range(20):      # (workspaces and outputs come and go on both streams)
+        got = te.te_rmsnorm_fwd(x, gamma, stream=side)
+        dgot = te.te_rmsnorm_bwd(x, x, got.rstd, gamma, stream=side)
+        noise = [torch.full_like(x, float("nan")) for _ in range(4)]
+        assert torch.cuda.current_stream() == before
+    side.synchronize()
+    del noise
+    assert torch.equal(got.y, want.y) and all(torch.equal(a, b) for a, b in zip(dgot, dwant))
+
+
 def test_other_stream_and_graph():
     rows, cols = 256, 1024
     g = gen(21)

@@ -300,6 +300,19 @@ def test_offsets_past_32_bits():
     assert torch.equal(da, db)
 
 
+def test_given_stream():
+    v = make_logits(5000, 40, torch.float32, 6)
+    want = te.te_moe_router_fwd(v, 4, loss=True)
+    dw = torch.ones((5000, 4), device="cuda")
+    dwant = te.te_moe_router_bwd(v, want.index, want.lse, d_weight=dw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = te.te_moe_router_fwd(v, 4, loss=True, stream=side)
+    dgot = te.te_moe_router_bwd(v, got.index, got.lse, d_weight=dw, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and torch.equal(dwant, dgot)
+
+
 def test_other_stream_and_graph():
     tokens, experts, k = 3000, 48, 4
     v = make_logits(tokens, experts, torch.bfloat16, 6)
