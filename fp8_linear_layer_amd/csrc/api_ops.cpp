@@ -14,6 +14,7 @@ using tefp8::report;
 using tefp8::report_ok;
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxCount = (int64_t)1 << 36;   // elements of a gradient: a batch's chunks are counted in 32 bits
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool is_fp8(te_dtype_t d) { return d == TE_DTYPE_E4M3 || d == TE_DTYPE_E5M2; }
@@ -369,6 +370,7 @@ te_status_t te_grad_norm_clip(const te_grad_tensor_t* tensors, int64_t n, float 
             if (!t.grad) return report(TE_ERR_INVALID_ARGUMENT, "%s: tensor %lld has a null gradient", fn, (long long)i);
             if (!aligned(t.grad, size_of(t.grad_dtype)) || (t.out && !aligned(t.out, size_of(t.out_dtype))))
                 return report(TE_ERR_MISALIGNED, "%s: tensor %lld is not aligned to its elements", fn, (long long)i);
+            if (t.count > kMaxCount) return report(TE_ERR_UNSUPPORTED, "%s: tensor %lld has more than 2^36 elements", fn, (long long)i);
             if (t.out == t.grad && t.out_dtype != t.grad_dtype)
                 return report(TE_ERR_INVALID_ARGUMENT, "%s: tensor %lld: in place needs one type", fn, (long long)i);
         }
@@ -382,7 +384,7 @@ te_status_t te_grad_norm_clip(const te_grad_tensor_t* tensors, int64_t n, float 
                 b.t[b.n] = tefp8::ClipTensor{t.grad, t.out, t.count};
                 b.first[b.n] = b.chunks;
                 b.types[b.n] = (t.grad_dtype == TE_DTYPE_BF16 ? 1 : 0) | (t.out_dtype == TE_DTYPE_BF16 ? 2 : 0);
-                b.chunks += tefp8::clip_chunks(t.count);
+                b.chunks += (int32_t)tefp8::clip_chunks(t.count);
                 ++b.n;
             }
             return at;

@@ -27,17 +27,24 @@ constexpr int64_t kChunk = 8192;   // elements
 template <class T> constexpr int kUnit = 16 / sizeof(typename T::store_t);
 template <class T> constexpr int kUnits = (int)(kChunk / kThreads / kUnit<T>);
 
-// The last tensor whose first chunk is at or before `chunk`.
-__device__ __forceinline__ int tensor_of(const ClipBatch& b, int64_t chunk)
-{
-    int lo = 0, hi = b.n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (b.first[mid] <= chunk) lo = mid;
-        else hi = mid;
+// Which tensor a chunk belongs to: the last whose first chunk is at or before it.  Every lane holds the first
+// chunks of two tensors, so a look-up is two votes; a binary search through the arguments waits for
+// memory at each of its steps.
+struct Tensors {
+    int32_t lo, hi;
+    __device__ __forceinline__ explicit Tensors(const ClipBatch& b)
+    {
+        static_assert(kClipBatch <= 128, "two tensors per lane");
+        const int lane = threadIdx.x & 63;
+        lo = lane < b.n ? b.first[lane] : INT32_MAX;
+        hi = 64 + lane < b.n ? b.first[64 + lane < kClipBatch ? 64 + lane : 0] : INT32_MAX;
     }
-    return lo;
-}
+    __device__ __forceinline__ int of(int32_t chunk) const
+    {
+        const int i = __popcll(__ballot(lo <= chunk)) + __popcll(__ballot(hi <= chunk)) - 1;
+        return __builtin_amdgcn_readfirstlane(i);
+    }
+};
 
 // What is far larger than the last cache is read and written past it (kStream): 470 million fp32 gradients
 // take 270 us instead of 335 in the first pass so.
@@ -122,9 +129,10 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const ClipBatch b,
 #pragma unroll
         for (float x : v) s += (double)x * (double)x;
     };
-    for (int64_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
-        const int i = tensor_of(b, c);
-        const int64_t first = (c - b.first[i]) * kChunk;
+    const Tensors tensors(b);
+    for (int32_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
+        const int i = tensors.of(c);
+        const int64_t first = (int64_t)(c - b.first[i]) * kChunk;
         if (b.types[i] & 1) each_unit<Bf16, kStream>(b.t[i], first, add);
         else each_unit<F32, kStream>(b.t[i], first, add);
     }
@@ -167,17 +175,18 @@ template <bool kStream>
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ClipBatch b, const double* __restrict__ partial,
                                                               int64_t slots, float max_norm, float* __restrict__ norm_out)
 {
+    const Tensors tensors(b);
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < slots; i += kThreads) s += partial[i];
     const float norm = (float)sqrt(block_sum(s));
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
     float coef = max_norm / (norm + 1e-6f);
     coef = coef > 1.0f ? 1.0f : coef;   // (NaN stays)
-    for (int64_t c = b.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-        const int i = tensor_of(b, c);
+    for (int32_t c = b.chunks - 1 - (int32_t)blockIdx.x; c >= 0; c -= gridDim.x) {
+        const int i = tensors.of(c);
         const ClipTensor& t = b.t[i];
         if (!t.out || (t.out == t.grad && coef == 1.0f)) continue;   // nothing to write, or nothing changes
-        const int64_t first = (c - b.first[i]) * kChunk;
+        const int64_t first = (int64_t)(c - b.first[i]) * kChunk;
         switch (b.types[i]) {
         case 0: scale_chunk<F32, F32, kStream>(t, first, coef); break;
         case 1: scale_chunk<Bf16, F32, kStream>(t, first, coef); break;
@@ -189,11 +198,11 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ClipBatch b,
 
 // Gradients of this many chunks (half a gigabyte in fp32) and more go past the caches: twice the last cache's
 // size, so that what a later kernel could still find there is kept.
-constexpr int64_t kStreamChunks = 16384;
+constexpr int32_t kStreamChunks = 16384;
 
 }  // namespace
 
-int64_t clip_blocks(const ClipBatch& b) { return std::max<int64_t>(1, std::min<int64_t>(b.chunks, kClipBlocks)); }
+int64_t clip_blocks(const ClipBatch& b) { return std::max(1, std::min(b.chunks, kClipBlocks)); }
 
 int64_t clip_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 

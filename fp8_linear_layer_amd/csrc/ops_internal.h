@@ -111,10 +111,9 @@ struct ClipTensor {
 };
 struct ClipBatch {
     ClipTensor t[kClipBatch];
-    int64_t first[kClipBatch];   // first chunk of each tensor
+    int32_t first[kClipBatch];   // first chunk of each tensor
     uint8_t types[kClipBatch];   // bit 0: bf16 gradient, bit 1: bf16 output
-    int32_t n;
-    int64_t chunks;
+    int32_t n, chunks;
 };
 int64_t clip_chunks(int64_t n);
 int64_t clip_blocks(const ClipBatch& b);

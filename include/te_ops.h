@@ -134,8 +134,8 @@ te_status_t te_moe_router_bwd(const void* logits, te_dtype_t logits_dtype, int64
  * finite gradients zero.
  *
  *  tensors       host array of n descriptors, read during the call; each tensor
- *                has `count` elements one after the other, aligned to an
- *                element.  out may be grad itself (same type: in place, and not
+ *                has `count` elements (at most 2^36) one after the other, aligned
+ *                to an element.  out may be grad itself (same type: in place, and not
  *                touched where the norm is at most max_norm) or null (only its
  *                part of the norm)
  *  max_norm      > 0

@@ -130,7 +130,7 @@ def clip(lib, tensors=((A, B, 100, F32, BF),), n=None, max_norm=1.0, norm=C, ws=
     (dict(tensors=((None, B, 5, F32, F32),)), INV), (dict(tensors=((A, B, -1, F32, F32),)), INV),
     (dict(tensors=((A, B, 5, E4, F32),)), INV), (dict(tensors=((A, B, 5, F32, 0),)), INV),
     (dict(tensors=((A, B, 5, BF, BF), (A + 1, B, 5, BF, BF))), MISAL), (dict(tensors=((A, B + 2, 5, F32, F32),)), MISAL),
-    (dict(tensors=((A, A, 5, F32, BF),)), INV),
+    (dict(tensors=((A, A, 5, F32, BF),)), INV), (dict(tensors=((A, B, (1 << 36) + 1, F32, F32),)), UNSUP),
 ])
 def test_clip_rejects(lib, kw, status):
     refused(lib, clip(lib, **kw), status)
