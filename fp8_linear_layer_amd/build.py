@@ -54,7 +54,7 @@ def _build_binding(verbose: bool) -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
            *[f"-isystem{p}" for p in [*include_paths(), sysconfig.get_paths()["include"], "/opt/rocm/include"]],
-           os.path.join(CSRC, "binding.cpp"), *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10",
+           os.path.join(CSRC, "binding.cpp"), *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10",
            "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -292,6 +292,9 @@ template <class Y, class H, bool kRes, int kTPR, int kNV>
 __global__ __launch_bounds__(kThreadsOf<kTPR>) void rmsnorm_bwd_kernel(const NormBwdArgs a)
 {
     constexpr int kRows = kThreadsOf<kTPR> / kTPR;
+    // Four chunks per thread do not fit the registers beside the sums for dgamma: such rows are read again
+    // after the reduction (838 x 20000 bf16: 150 us with the registers spilled).
+    constexpr bool kTwice = kNV == 4;
     __shared__ float red[2][kThreadsOf<kTPR> / 64];
     __shared__ float slots[kRows > 1 ? kRows : 1][kRows > 1 ? kTPR * 8 : 1];
     const int t = threadIdx.x % kTPR, slot = threadIdx.x / kTPR, cols = a.cols;
@@ -312,16 +315,23 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void rmsnorm_bwd_kernel(const Nor
         const int64_t row = in ? base + slot : a.rows - 1;
         const auto* dy = static_cast<const typename Y::store_t*>(a.dy) + row * a.ld_dy;
         const auto* h = static_cast<const typename H::store_t*>(a.h) + row * a.ld_h;
+        const auto* res = static_cast<const typename H::store_t*>(a.dres) + (kRes ? row * a.ld_dres : 0);
         Raw8<Y> ry[kNV];
         Raw8<H> rh[kNV], rr[kNV];
-        load_row(ry, dy, c, cols, false);
-        load_row(rh, h, c, cols, false);
-        if constexpr (kRes)
-            load_row(rr, static_cast<const typename H::store_t*>(a.dres) + row * a.ld_dres, c, cols, false);
+        if constexpr (!kTwice) {
+            load_row(ry, dy, c, cols, false);
+            load_row(rh, h, c, cols, false);
+            if constexpr (kRes) load_row(rr, res, c, cols, false);
+        }
         const float rstd = a.rstd[row];
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
+            if constexpr (kTwice) {
+                ry[i] = load_chunk<Y>(dy, c[i], cols);
+                rh[i] = load_chunk<H>(h, c[i], cols);
+                rg[i] = load_chunk<Bf16>(a.gamma, c[i], cols);
+            }
             float dyv[8], hv[8], g[8];
             unpack8(ry[i], dyv);
             unpack8(rh[i], hv);
@@ -340,6 +350,13 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void rmsnorm_bwd_kernel(const Nor
         if (!in) continue;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
+            if constexpr (kTwice) {
+                asm volatile("" ::: "memory");   // (loaded here again, not kept)
+                ry[i] = load_chunk<Y>(dy, c[i], cols);
+                rh[i] = load_chunk<H>(h, c[i], cols);
+                rg[i] = load_chunk<Bf16>(a.gamma, c[i], cols);
+                if constexpr (kRes) rr[i] = load_chunk<H>(res, c[i], cols);
+            }
             float dyv[8], hv[8], g[8], d[8], r[8] = {};
             unpack8(ry[i], dyv);
             unpack8(rh[i], hv);
@@ -347,7 +364,16 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void rmsnorm_bwd_kernel(const Nor
             if constexpr (kRes) unpack8(rr[i], r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[j] = rstd * (dyv[j] * g[j] - hv[j] * rstd * mean) + r[j];
-            store_chunk(static_cast<typename H::store_t*>(a.dh) + row * a.ld_dh, c[i], cols, pack8(H{}, d));
+            auto* out = static_cast<typename H::store_t*>(a.dh) + row * a.ld_dh;
+            if (kTwice && c[i].skip > 0) {
+                // (dh may be dres, which the neighbour reads for itself only now)
+                if (c[i].on)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= c[i].skip) store_one(out + c[i].c0 + j, pack8(H{}, d), j);
+            } else {
+                store_chunk(out, c[i], cols, pack8(H{}, d));
+            }
         }
     }
     if (!a.partial) return;   // no dgamma wanted
@@ -417,6 +443,7 @@ template <template <int, int> class F, class A>
 void by_cols(const A& a, hipStream_t stream)
 {
     if (a.cols <= 128) F<16, 1>::run(a, stream);
+    else if (a.cols <= 256) F<32, 1>::run(a, stream);
     else if (a.cols <= 512) F<64, 1>::run(a, stream);
     else if (a.cols <= 1024) F<128, 1>::run(a, stream);
     else if (a.cols <= 2048) F<256, 1>::run(a, stream);
@@ -427,7 +454,7 @@ void by_cols(const A& a, hipStream_t stream)
 }
 int threads_per_row(int64_t cols)
 {
-    return cols <= 128 ? 16 : cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
+    return cols <= 128 ? 16 : cols <= 256 ? 32 : cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
 }
 
 // Inputs of this many bytes are read past the caches, so that h and the outputs stay in the last one.  Forward

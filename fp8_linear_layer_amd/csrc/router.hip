@@ -376,13 +376,14 @@ __global__ __launch_bounds__(kFwdThreads, (kFwdWavesPerSimd<T, kNC, kK>)) void r
                 col[q] = p == i ? top.column(q * kL + i) : col[q];
             }
             const bool chosen = sent && key > kClosed && q * kL + p < min(k, kK);
-            ev[q] = chosen ? expf(from_order_key(key) - m) : 0.0f;
+            ev[q] = chosen ? exp_exact(from_order_key(key) - m) : 0.0f;
             if (!chosen) col[q] = -1;
             sum += ev[q];
         }
-        const float inv = 1.0f / s;
+        // (the hardware's reciprocal, one step of 2^-23 off at most: the sums are no better)
+        const float inv = __builtin_amdgcn_rcpf(s);
         float scale = inv;
-        if (a.renorm) scale = s == s ? 1.0f / sum_lanes<kL>(sum) : s;
+        if (a.renorm) scale = s == s ? __builtin_amdgcn_rcpf(sum_lanes<kL>(sum)) : s;
 #pragma unroll
         for (int q = 0; q < kOwn; ++q) {
             const int j = q * kL + p;
@@ -578,11 +579,13 @@ __global__ __launch_bounds__(kThreads, 4) void router_bwd_kernel(const RouterBwd
     if (a.d_loss) {
         const float n = (float)max(a.routed[0], 1);
         const float f = a.d_loss[0] * ((float)E / (float)k) / (n * n);
-        // (past the last column any count will do: p is zero there)
+        // (read as the logits are; past the last column any count will do, as p is zero there)
+        Raw8<F32> c[kNC];
+        load_logits<F32, kL>(c, reinterpret_cast<const float*>(a.counts), p, E);
 #pragma unroll
         for (int i = 0; i < kNC; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g[i][j] = f * (float)a.counts[min((i * kL + p) * 8 + j, E - 1)];
+            for (int j = 0; j < 8; ++j) g[i][j] = f * (float)(int32_t)(j < 4 ? (uint32_t)c[i].a[j & 3] : (uint32_t)c[i].b[j & 3]);
     }
 
     const auto* logits = static_cast<const typename T::store_t*>(a.logits);
@@ -687,16 +690,18 @@ __global__ __launch_bounds__(kThreads, 4) void router_bwd_kernel(const RouterBwd
 }
 
 // Lanes per token and chunks per lane for a number of experts: as few lanes as hold the row with
-// at most four chunks each, and eight lanes (one 128-byte line of bf16 per chunk) beyond 16 experts.
+// at most four chunks each, and at least eight (one 128-byte line of bf16 per chunk) beyond 32 experts.
 struct Shape { int lanes, chunks; };
 Shape shape_of(int64_t experts)
 {
     if (experts <= 8) return {1, 1};
     if (experts <= 16) return {1, 2};
+    if (experts <= 32) return {4, 1};
     if (experts <= 64) return {8, 1};
     if (experts <= 128) return {8, 2};
     if (experts <= 256) return {8, 4};
     if (experts <= 512) return {16, 4};
+    if (experts <= 1024) return {32, 4};
     return {64, 4};
 }
 
@@ -742,10 +747,12 @@ hipError_t bwd_run(const RouterBwdArgs& a, hipStream_t stream)
         const Shape s = shape_of((a).experts);                     \
         if (s.lanes == 1 && s.chunks == 1) return F<T, 1, 1>(a, stream); \
         if (s.lanes == 1) return F<T, 1, 2>(a, stream);            \
+        if (s.lanes == 4) return F<T, 4, 1>(a, stream);            \
         if (s.lanes == 8 && s.chunks == 1) return F<T, 8, 1>(a, stream); \
         if (s.lanes == 8 && s.chunks == 2) return F<T, 8, 2>(a, stream); \
         if (s.lanes == 8) return F<T, 8, 4>(a, stream);            \
         if (s.lanes == 16) return F<T, 16, 4>(a, stream);          \
+        if (s.lanes == 32) return F<T, 32, 4>(a, stream);          \
         return F<T, 64, 4>(a, stream);                             \
     } while (0)
 
@@ -754,14 +761,17 @@ template <class T> hipError_t bwd_shape(const RouterBwdArgs& a, hipStream_t stre
 
 }  // namespace
 
-// Workgroups: one where it takes the tokens in at most four steps and the counts are asked for (no
-// second kernel then), else up to 512 of them.
+// Workgroups: one where it takes the tokens in at most four steps and the counts are asked for (no second
+// kernel then).  Else as many as are resident, and with four chunks per lane half of that: those are bound
+// by their instructions, and every workgroup costs the second kernel a row (16384 x 512 bf16, both kernels: 17.1
+// us with 256 workgroups, 19.6 with 512; 100000 x 64 fp32: 30.2 and 27.3).
 int64_t router_fwd_blocks(int64_t tokens, int64_t experts, bool loss)
 {
-    const int64_t per = kFwdWaves * (64 / shape_of(experts).lanes);
+    const Shape s = shape_of(experts);
+    const int64_t per = kFwdWaves * (64 / s.lanes);
     const int64_t blocks = (tokens + per - 1) / per;
     if (loss && blocks <= 4) return 1;
-    return std::min<int64_t>(blocks, loss ? 512 : 4096);
+    return std::min<int64_t>(blocks, !loss ? 4096 : s.chunks == 4 ? 256 : 512);
 }
 
 int64_t router_fwd_workspace_bytes(int64_t tokens, int64_t experts)

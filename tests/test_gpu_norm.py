@@ -84,7 +84,7 @@ def check_fwd(x, res, gamma, r):
     return y
 
 
-COLS = [1, 2, 7, 8, 9, 15, 64, 129, 250, 512, 513, 1000, 2048, 2056, 2112, 4096, 4097, 7168, 8192, 8200, 14336, 16384, 16392, 32768]
+COLS = [1, 2, 7, 8, 9, 15, 64, 129, 250, 256, 257, 512, 513, 1000, 2048, 2056, 2112, 4096, 4097, 7168, 8192, 8200, 14336, 16384, 16392, 20003, 32768]
 
 
 @pytest.mark.parametrize("cols", COLS)
@@ -233,7 +233,7 @@ def test_backward(cols, yt, ht, res):
         assert none is None and torch.equal(dh, dh3)
 
 
-@pytest.mark.parametrize("cols,ld,shift", [(250, 253, 1), (2112, 2117, 3), (5, 7, 1), (4096, 4099, 5)])
+@pytest.mark.parametrize("cols,ld,shift", [(250, 253, 1), (2112, 2117, 3), (5, 7, 1), (4096, 4099, 5), (20003, 20011, 1), (32768, 32768, 0)])
 @pytest.mark.parametrize("t", ["bf16", "f32"])
 def test_backward_strides_and_in_place(cols, ld, shift, t):
     rows = 41

@@ -74,7 +74,7 @@ def check_fwd(r, e, loss=True):
         assert abs(float(r.loss) - e["loss"]) <= 256 * U * e["loss"]
 
 
-EXPERTS = [1, 2, 3, 7, 8, 9, 12, 16, 17, 31, 40, 64, 65, 77, 128, 129, 200, 256, 257, 400, 511, 512, 513, 1000, 2048]
+EXPERTS = [1, 2, 3, 7, 8, 9, 12, 16, 17, 31, 32, 33, 40, 64, 65, 77, 128, 129, 200, 256, 257, 400, 511, 512, 513, 1000, 1024, 1025, 2048]
 
 
 @pytest.mark.parametrize("experts", EXPERTS)
