@@ -8,7 +8,8 @@
 // device first.  The first kernel leaves one sum of squares per workgroup, in fp64 (a square of an
 // fp32 gradient need not fit fp32's range); in the second every workgroup adds those up in the same
 // fixed order, which costs less than a launch between the two.  The second goes through the chunks
-// backwards: what the first read last is what the caches still hold.
+// backwards: what the first read last is what the caches still hold (with gradients many times their size
+// the order makes no difference).
 //
 // Measured with 470 million fp32 gradients into bf16: 270 us (7.0 TB/s) and 508 us (5.5 TB/s).
 #include <hip/hip_runtime.h>
