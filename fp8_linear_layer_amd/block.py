@@ -44,8 +44,10 @@ class _RmsNormFn(torch.autograd.Function):
         h, rstd, gamma = ctx.saved_tensors
         if dy is None:      # only h was used
             return (dh_next.to(ctx.x_dtype) if dh_next is not None else None), dh_next, None, None
-        dh, dgamma = te_rmsnorm_bwd(dy.contiguous(), h, rstd, gamma, dres=dh_next.contiguous() if dh_next is not None else None)
-        return dh.to(ctx.x_dtype), (dh if ctx.added else None), _to_param(dgamma, gamma), None
+        train = ctx.needs_input_grad[2]      # a frozen weight: no sums, and nothing added to its main_grad
+        dh, dgamma = te_rmsnorm_bwd(dy.contiguous(), h, rstd, gamma, dres=dh_next.contiguous() if dh_next is not None else None,
+                                    need_dgamma=train)
+        return dh.to(ctx.x_dtype), (dh if ctx.added else None), (_to_param(dgamma, gamma) if train else None), None
 
 
 class RmsNorm(torch.nn.Module):
@@ -78,7 +80,8 @@ class _Fp8NormMlpFn(torch.autograd.Function):
         H, N = w1.shape[0], w2.shape[0]
         _check_dims(M, K, H, N)
         flags, accum = _fwd_policy(pow2)
-        n = te_rmsnorm_fwd(x, gamma, eps, residual=residual, out_dtype=FWD_DTYPE, flags=flags, transpose=True)
+        # (the transposed operand is for fc1's weight gradient alone)
+        n = te_rmsnorm_fwd(x, gamma, eps, residual=residual, out_dtype=FWD_DTYPE, flags=flags, transpose=ctx.needs_input_grad[4])
         h = x if residual is None else n.h
         qw1, sw1, _, _ = c1.get(w1)
         z1 = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
@@ -97,24 +100,39 @@ class _Fp8NormMlpFn(torch.autograd.Function):
         h, rstd, gamma, qnt, snt, z1, qat, sat, w1, w2 = ctx.saved_tensors
         if dy is None:      # only h was used
             return (dh_next.to(ctx.x_dtype) if dh_next is not None else None), dh_next, *[None] * 9
+        # What is frozen gets no product, no sum, and nothing added to its main_grad.
+        need_x, need_res, need_gamma, _, need_w1, need_b1, need_w2, need_b2 = ctx.needs_input_grad[:8]
+        through = need_x or need_res or need_gamma      # the gradient goes on below fc1
+        d_x = d_res = d_gamma = d_w1 = d_b1 = d_w2 = d_b2 = None
         qdy, sdy, qdyt, sdyt = te_cast_fp8_per_token_transpose(dy.contiguous(), BWD_DTYPE)
-        w2buf, f2 = _grad_buffer(w2)
-        db2 = torch.empty((w2.shape[0],), dtype=torch.float32, device=dy.device)
-        te_fp8_wgrad_accum_bgrad(qdyt, sdyt, BWD_DTYPE, qat, sat, FWD_DTYPE, w2buf, db2, TE_ACCUM_FULL_FP32)
-        _, _, qw2t, sw2t = ctx.c2.get(w2)
-        db1 = torch.empty((w1.shape[0],), dtype=torch.float32, device=dy.device)
-        dz1 = te_fp8_gemm_dgrad_deterministic(qdy, sdy, BWD_DTYPE, qw2t, sw2t, FWD_DTYPE, db1,
-                                              epilogue=TE_EPI_DGELU | TE_EPI_BGRAD, preact=z1, dx_dtype=TE_DTYPE_BF16,
-                                              accum=TE_ACCUM_FULL_FP32)
-        qdz, sdz, qdzt, sdzt = te_cast_fp8_per_token_transpose(dz1, BWD_DTYPE)
-        w1buf, f1 = _grad_buffer(w1)
-        te_fp8_wgrad_accum(qdzt, sdzt, BWD_DTYPE, qnt, snt, FWD_DTYPE, w1buf, TE_ACCUM_FULL_FP32)
-        _, _, qw1t, sw1t = ctx.c1.get(w1)
-        dn = te_fp8_gemm_dgrad(qdz, sdz, BWD_DTYPE, qw1t, sw1t, FWD_DTYPE, dx_dtype=TE_DTYPE_BF16, accum=TE_ACCUM_FULL_FP32)
-        dh, dgamma = te_rmsnorm_bwd(dn, h, rstd, gamma, dres=dh_next.contiguous() if dh_next is not None else None)
-        return (dh.to(ctx.x_dtype), dh if ctx.added else None, _to_param(dgamma, gamma), None,
-                None if f1 else w1buf.to(w1.dtype), db1.to(torch.bfloat16), None if f2 else w2buf.to(w2.dtype),
-                db2.to(torch.bfloat16), None, None, None)
+        if need_w2 or need_b2:
+            # (the bias gradient comes with the product: beside a frozen weight that goes to memory that nobody reads)
+            w2buf, f2 = _grad_buffer(w2) if need_w2 else (torch.empty(w2.shape, dtype=torch.float32, device=dy.device), True)
+            db2 = torch.empty((w2.shape[0],), dtype=torch.float32, device=dy.device)
+            te_fp8_wgrad_accum_bgrad(qdyt, sdyt, BWD_DTYPE, qat, sat, FWD_DTYPE, w2buf, db2, TE_ACCUM_FULL_FP32)
+            d_w2 = None if f2 else w2buf.to(w2.dtype)
+            d_b2 = db2.to(torch.bfloat16) if need_b2 else None
+        if through or need_w1 or need_b1:
+            _, _, qw2t, sw2t = ctx.c2.get(w2)
+            db1 = torch.empty((w1.shape[0],), dtype=torch.float32, device=dy.device)
+            dz1 = te_fp8_gemm_dgrad_deterministic(qdy, sdy, BWD_DTYPE, qw2t, sw2t, FWD_DTYPE, db1,
+                                                  epilogue=TE_EPI_DGELU | TE_EPI_BGRAD, preact=z1, dx_dtype=TE_DTYPE_BF16,
+                                                  accum=TE_ACCUM_FULL_FP32)
+            d_b1 = db1.to(torch.bfloat16) if need_b1 else None
+        if through or need_w1:
+            qdz, sdz, qdzt, sdzt = te_cast_fp8_per_token_transpose(dz1, BWD_DTYPE)
+        if need_w1:
+            w1buf, f1 = _grad_buffer(w1)
+            te_fp8_wgrad_accum(qdzt, sdzt, BWD_DTYPE, qnt, snt, FWD_DTYPE, w1buf, TE_ACCUM_FULL_FP32)
+            d_w1 = None if f1 else w1buf.to(w1.dtype)
+        if through:
+            _, _, qw1t, sw1t = ctx.c1.get(w1)
+            dn = te_fp8_gemm_dgrad(qdz, sdz, BWD_DTYPE, qw1t, sw1t, FWD_DTYPE, dx_dtype=TE_DTYPE_BF16, accum=TE_ACCUM_FULL_FP32)
+            dh, dgamma = te_rmsnorm_bwd(dn, h, rstd, gamma, dres=dh_next.contiguous() if dh_next is not None else None,
+                                        need_dgamma=need_gamma)
+            d_x, d_res = dh.to(ctx.x_dtype), dh if ctx.added else None
+            d_gamma = _to_param(dgamma, gamma) if need_gamma else None
+        return d_x, d_res, d_gamma, None, d_w1, d_b1, d_w2, d_b2, None, None, None
 
 
 class Fp8NormMlp(torch.nn.Module):

@@ -1,0 +1,203 @@
+"""The modules' own logic (block.py, linear.py) on the CPU, with torch in the place of the library's calls: which
+gradients a backward pass computes and accumulates, and what clip_grad_norm takes.
+
+The stand-ins keep the calls' signatures and layouts and leave out the 8-bit rounding, so that gradients can be
+compared with autograd's (bf16 stores: a few half steps of 2^-8)."""
+import math
+
+import pytest
+import torch
+
+te = pytest.importorskip("fp8_linear_layer_amd")
+from fp8_linear_layer_amd import block, linear  # noqa: E402
+from fp8_linear_layer_amd.ops import RmsNormOutput, RouterOutput  # noqa: E402
+
+
+class Calls:
+    """The library's calls in torch; `log` has their names, `options` what a call was asked for beside its operands."""
+
+    def __init__(self):
+        self.log, self.options = [], []
+
+    def said(self, name, **options):
+        self.log.append(name)
+        self.options.append(dict(name=name, **options))
+
+    def te_rmsnorm_fwd(self, x, gamma, eps=1e-5, residual=None, out_dtype=te.TE_DTYPE_BF16, flags=0, transpose=False):
+        self.said("norm", transpose=transpose)
+        h = (x.float() + residual.float()).to(residual.dtype) if residual is not None else None
+        v = (h if h is not None else x).float()
+        rstd = torch.rsqrt((v * v).mean(1) + eps)
+        y = v * rstd[:, None] * gamma.float()
+        fp8 = out_dtype not in (te.TE_DTYPE_BF16, te.TE_DTYPE_F32)
+        return RmsNormOutput(h, rstd, None if fp8 else y.bfloat16(), y if fp8 else None, None,
+                             y.t().contiguous() if transpose else None, None)
+
+    def te_rmsnorm_bwd(self, dy, h, rstd, gamma, dres=None, need_dgamma=True):
+        self.said("norm_bwd", need_dgamma=need_dgamma)
+        xh, g = h.float() * rstd[:, None], dy.float() * gamma.float()
+        dh = rstd[:, None] * (g - xh * (g * xh).mean(1, keepdim=True)) + (0 if dres is None else dres.float())
+        return dh.to(h.dtype), (dy.float() * xh).sum(0) if need_dgamma else None
+
+    def te_cast_fp8_per_token_transpose(self, x, dtype, flags=0):
+        self.said("cast")
+        return x.float(), None, x.float().t().contiguous(), None
+
+    def te_fp8_gemm_fwd(self, a, sa, da, b, sb, db, bias=None, epilogue=0, preact=None, y_dtype=None, accum=0):
+        self.said("fwd")
+        z = a @ b.t() + (0 if bias is None else bias.float())
+        if preact is not None:
+            preact.copy_(z)
+        return (torch.nn.functional.gelu(z, approximate="tanh") if epilogue & te.TE_EPI_GELU else z).bfloat16()
+
+    def te_fp8_gemm_dgrad(self, a, sa, da, b, sb, db, epilogue=0, preact=None, dx_dtype=None, accum=0):
+        self.said("dgrad")
+        return self._dgrad(a, b, preact).bfloat16()
+
+    def te_fp8_gemm_dgrad_deterministic(self, a, sa, da, b, sb, db, bias_grad, epilogue=0, preact=None, dx_dtype=None, accum=0):
+        self.said("dgrad")
+        d = self._dgrad(a, b, preact)
+        bias_grad.copy_(d.sum(0))
+        return d.bfloat16()
+
+    def _dgrad(self, a, b, preact):
+        d = a @ b.t()
+        if preact is not None:
+            with torch.enable_grad():
+                z = preact.float().requires_grad_()
+                torch.nn.functional.gelu(z, approximate="tanh").sum().backward()
+            d = d * z.grad
+        return d
+
+    def te_fp8_wgrad_accum(self, a, sa, da, b, sb, db, out, accum):
+        self.said("wgrad")
+        out += a @ b.t()
+
+    def te_fp8_wgrad_accum_bgrad(self, a, sa, da, b, sb, db, out, bias_grad, accum):
+        self.said("wgrad")
+        out += a @ b.t()
+        bias_grad.copy_(a.sum(1))
+
+    def te_moe_router_fwd(self, logits, top_k, renormalize=False, token_mask=None, loss=False, need_lse=None):
+        p = torch.softmax(logits.float(), 1)
+        w, index = p.topk(top_k, 1)
+        counts = torch.bincount(index.reshape(-1), minlength=p.shape[1]).int()
+        return RouterOutput(index.int(), w, torch.logsumexp(logits.float(), 1), counts, torch.tensor([len(p)], dtype=torch.int32),
+                            (counts * p.sum(0)).sum().reshape(1) * p.shape[1] / (top_k * len(p) ** 2))
+
+    def te_moe_router_bwd(self, logits, index, lse, counts=None, routed=None, d_weight=None, d_loss=None, renormalize=False):
+        p = torch.exp(logits.float() - lse[:, None])
+        b = torch.zeros_like(p)
+        if d_loss is not None:
+            b += d_loss * p.shape[1] / index.shape[1] * counts.float() / len(p) ** 2
+        if d_weight is not None:
+            b.scatter_add_(1, index.long(), d_weight)
+        return (p * (b - (p * b).sum(1, keepdim=True))).to(logits.dtype)
+
+    def te_grad_norm_clip(self, grads, max_norm):
+        self.said("clip", count=len(grads))
+        norm = torch.sqrt(sum((g.double() ** 2).sum() for g in grads)).float().reshape(1)
+        for g in grads:
+            g.mul_(min(1.0, max_norm / (float(norm) + 1e-6)))
+        return norm
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    c = Calls()
+    for module in (block, linear):
+        for name in dir(c):
+            if name.startswith("te_") and hasattr(module, name):
+                monkeypatch.setattr(module, name, getattr(c, name))
+    return c
+
+
+def randn(shape, seed, std=1.0, dtype=torch.bfloat16):
+    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * std).to(dtype)
+
+
+def close(a, b):
+    """Within eight half steps of bf16 of the largest value (the intermediate results are stored in bf16)."""
+    return bool(((a.double() - b.double()).abs() <= 8 * 2.0 ** -8 * b.double().abs().max()).all())
+
+
+def norm_mlp(main_grad=True):
+    m = block.Fp8NormMlp(128, 256, 128, device="cpu", generator=torch.Generator().manual_seed(0))
+    m.mlp.b1.data.copy_(randn((256,), 5, 0.1))
+    m.mlp.b2.data.copy_(randn((128,), 6, 0.1))
+    if not main_grad:
+        for p in (m.norm.weight, m.mlp.w1, m.mlp.w2):
+            del p.main_grad
+    return m
+
+
+PARAMS = ("norm.weight", "mlp.w1", "mlp.b1", "mlp.w2", "mlp.b2")
+
+
+def got(p):
+    main = getattr(p, "main_grad", None)
+    return main if main is not None else p.grad
+
+
+def reference(m, x, res, dy, dh):
+    """Gradients by autograd of the block in fp32: x, residual and the parameters."""
+    leaves = [t.detach().float().requires_grad_() for t in (x, res, *(m.get_parameter(n) for n in PARAMS))]
+    x32, r32, g, w1, b1, w2, b2 = leaves
+    h = x32 + r32
+    n = h * torch.rsqrt((h * h).mean(1, keepdim=True) + 1e-5) * g
+    y = torch.nn.functional.gelu(n @ w1.t() + b1, approximate="tanh") @ w2.t() + b2
+    torch.autograd.backward([y, h], [dy.float(), dh.float()])
+    return [t.grad for t in leaves]
+
+
+# ------------------------------------------------------------------ frozen parameters
+@pytest.mark.parametrize("main_grad", [False, True])
+def test_a_frozen_norm_weight_gets_no_gradient(calls, main_grad):
+    m = block.RmsNorm(64, device="cpu", main_grad=main_grad)
+    m.weight.requires_grad_(False)
+    x = randn((6, 64), 1).requires_grad_()
+    y, _ = m(x)
+    y.backward(randn(y.shape, 2))
+    assert x.grad is not None and m.weight.grad is None
+    assert not main_grad or bool((m.weight.main_grad == 0).all())
+    assert [o["need_dgamma"] for o in calls.options if o["name"] == "norm_bwd"] == [False]
+
+
+@pytest.mark.parametrize("main_grad", [False, True])
+@pytest.mark.parametrize("frozen", [(), ("norm.weight",), ("mlp.w1",), ("mlp.w2",), ("mlp.w1", "mlp.w2"), ("mlp.b1", "mlp.b2"),
+                                    ("mlp.w1", "mlp.b1"), ("mlp.w2", "mlp.b2"), PARAMS, PARAMS[:4], PARAMS[1:], PARAMS[:1] + PARAMS[2:]],
+                         ids="+".join)
+@pytest.mark.parametrize("inputs", [True, False])
+def test_norm_mlp_with_frozen_parameters(calls, frozen, inputs, main_grad):
+    """Every gradient that is asked for, and nothing added to what is frozen."""
+    if not inputs and set(frozen) == set(PARAMS):
+        pytest.skip("nothing takes a gradient")
+    m = norm_mlp(main_grad)
+    for n in frozen:
+        m.get_parameter(n).requires_grad_(False)
+    x, res = randn((128, 128), 1).requires_grad_(inputs), randn((128, 128), 2).requires_grad_(inputs)
+    y, h = m(x, res)
+    dy, dh = randn(y.shape, 3, 0.1), randn(h.shape, 4, 0.1)
+    want = reference(m, x, res, dy, dh)
+    del calls.log[:], calls.options[:]
+    torch.autograd.backward([y, h], [dy, dh]) if h.requires_grad else y.backward(dy)
+    if inputs:
+        assert close(x.grad, want[0]) and close(res.grad, want[1])
+    for n, w in zip(PARAMS, want[2:]):
+        p = m.get_parameter(n)
+        if n in frozen:
+            assert p.grad is None and bool((getattr(p, "main_grad", torch.zeros(1)) == 0).all()), n
+        else:
+            assert close(got(p), w), n
+    assert [o["need_dgamma"] for o in calls.options if o["name"] == "norm_bwd"] in ([], ["norm.weight" not in frozen])
+    # products of the weights' gradients: of those that are asked for (fc2's brings its bias gradient)
+    assert calls.log.count("wgrad") == ("mlp.w1" not in frozen) + (not {"mlp.w2", "mlp.b2"} <= set(frozen))
+
+
+def test_a_frozen_fc1_needs_no_transposed_operand(calls):
+    m = norm_mlp()
+    x = randn((128, 128), 1).requires_grad_()
+    m(x)
+    m.mlp.w1.requires_grad_(False)
+    m(x)
+    assert [o["transpose"] for o in calls.options if o["name"] == "norm"] == [True, False]
