@@ -201,3 +201,16 @@ def test_a_frozen_fc1_needs_no_transposed_operand(calls):
     m.mlp.w1.requires_grad_(False)
     m(x)
     assert [o["transpose"] for o in calls.options if o["name"] == "norm"] == [True, False]
+
+
+# ------------------------------------------------------------------ clip_grad_norm
+def test_clip_leaves_frozen_parameters_out(calls):
+    """A frozen parameter's buffer (here one filled before it was frozen) neither counts nor changes."""
+    a, b, c = (torch.nn.Parameter(torch.zeros(4, dtype=torch.bfloat16)) for _ in range(3))
+    a.main_grad, b.main_grad = torch.full((4,), 3.0), torch.full((4,), 100.0)
+    b.requires_grad_(False)
+    c.grad = torch.full((4,), 100.0, dtype=torch.bfloat16)
+    c.requires_grad_(False)
+    norm = block.clip_grad_norm([a, b, c], 3.0)
+    assert float(norm) == 6.0
+    assert torch.allclose(a.main_grad, torch.full((4,), 1.5)) and bool((b.main_grad == 100).all()) and bool((c.grad == 100).all())
