@@ -214,3 +214,12 @@ def test_clip_leaves_frozen_parameters_out(calls):
     norm = block.clip_grad_norm([a, b, c], 3.0)
     assert float(norm) == 6.0
     assert torch.allclose(a.main_grad, torch.full((4,), 1.5)) and bool((b.main_grad == 100).all()) and bool((c.grad == 100).all())
+
+
+def test_clip_takes_a_shared_parameter_once(calls):
+    """A weight that two modules share comes twice in their parameters: clipped twice, its two passes would race."""
+    a, b = (torch.nn.Parameter(torch.zeros(4, dtype=torch.bfloat16)) for _ in range(2))
+    a.main_grad, b.main_grad = torch.full((4,), 3.0), torch.full((4,), 4.0)
+    norm = block.clip_grad_norm([a, b, a], 5.0)
+    assert float(norm) == 10.0 and calls.options[-1]["count"] == 2
+    assert torch.allclose(a.main_grad, torch.full((4,), 1.5)) and torch.allclose(b.main_grad, torch.full((4,), 2.0))
