@@ -186,9 +186,10 @@ class TopKRouter(torch.nn.Module):
 
 
 def clip_grad_norm(parameters, max_norm):
-    """Clips the gradients of the parameters in place (main_grad where a parameter has one, else grad) to
+    """Clips the gradients of the parameters (or of one) in place (main_grad where a parameter has one, else grad) to
     a global norm of at most max_norm and returns the norm, fp32 [1] on the GPU.  Frozen parameters
     (requires_grad False) do not count and are left alone; one that comes several times counts once."""
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
     trained = {id(p): p for p in parameters if p.requires_grad}.values()
     grads = [getattr(p, "main_grad", None) if getattr(p, "main_grad", None) is not None else p.grad for p in trained]
     return te_grad_norm_clip([g for g in grads if g is not None], max_norm)

@@ -223,3 +223,10 @@ def test_clip_takes_a_shared_parameter_once(calls):
     norm = block.clip_grad_norm([a, b, a], 5.0)
     assert float(norm) == 10.0 and calls.options[-1]["count"] == 2
     assert torch.allclose(a.main_grad, torch.full((4,), 1.5)) and torch.allclose(b.main_grad, torch.full((4,), 2.0))
+
+
+def test_clip_takes_one_parameter_for_a_list(calls):
+    """As torch's function does; its rows, taken for parameters, have no gradients, and nothing was clipped."""
+    a = torch.nn.Parameter(torch.zeros(4, 4, dtype=torch.bfloat16))
+    a.main_grad = torch.full((4, 4), 2.0)
+    assert float(block.clip_grad_norm(a, 4.0)) == 8.0 and torch.allclose(a.main_grad, torch.ones(4, 4))
