@@ -17,7 +17,7 @@ from . import (TE_ACCUM_FULL_FP32, TE_DTYPE_BF16, TE_EPI_AUX_PREACT, TE_EPI_BGRA
                te_cast_fp8_per_token_transpose, te_fp8_gemm_dgrad, te_fp8_gemm_dgrad_deterministic, te_fp8_gemm_fwd,
                te_fp8_wgrad_accum, te_fp8_wgrad_accum_bgrad, te_grad_norm_clip, te_moe_router_bwd, te_moe_router_fwd,
                te_rmsnorm_bwd, te_rmsnorm_fwd)
-from .linear import BWD_DTYPE, FWD_DTYPE, Fp8Mlp, _check_dims, _fwd_policy, _grad_buffer
+from .linear import BWD_DTYPE, FWD_DTYPE, Fp8Mlp, _check_dims, _fwd_policy, _grad_buffer, _unread
 
 
 def _to_param(grad32, param):
@@ -106,8 +106,7 @@ class _Fp8NormMlpFn(torch.autograd.Function):
         d_x = d_res = d_gamma = d_w1 = d_b1 = d_w2 = d_b2 = None
         qdy, sdy, qdyt, sdyt = te_cast_fp8_per_token_transpose(dy.contiguous(), BWD_DTYPE)
         if need_w2 or need_b2:
-            # (the bias gradient comes with the product: beside a frozen weight that goes to memory that nobody reads)
-            w2buf, f2 = _grad_buffer(w2) if need_w2 else (torch.empty(w2.shape, dtype=torch.float32, device=dy.device), True)
+            w2buf, f2 = _grad_buffer(w2) if need_w2 else (_unread(w2), True)
             db2 = torch.empty((w2.shape[0],), dtype=torch.float32, device=dy.device)
             te_fp8_wgrad_accum_bgrad(qdyt, sdyt, BWD_DTYPE, qat, sat, FWD_DTYPE, w2buf, db2, TE_ACCUM_FULL_FP32)
             d_w2 = None if f2 else w2buf.to(w2.dtype)

@@ -99,6 +99,11 @@ def _grad_buffer(weight: torch.Tensor):
     return torch.zeros(weight.shape, dtype=torch.float32, device=weight.device), False
 
 
+def _unread(weight: torch.Tensor):
+    """Memory for a frozen weight's gradient, which nobody reads: its bias gradient comes with that product."""
+    return torch.empty(weight.shape, dtype=torch.float32, device=weight.device)
+
+
 class _Fp8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, cache: Fp8WeightCache, keep: dict | None, pow2: bool):
@@ -122,21 +127,25 @@ class _Fp8LinearFn(torch.autograd.Function):
         qxt, sxt, weight = ctx.saved_tensors
         dy = dy.contiguous()
         qdy, sdy, qdyt, sdyt = te_cast_fp8_per_token_transpose(dy, BWD_DTYPE)
-        _, _, qwt, swt = ctx.cache.get(weight)
-        dx = te_fp8_gemm_dgrad(qdy, sdy, BWD_DTYPE, qwt, swt, FWD_DTYPE, dx_dtype=TE_DTYPE_BF16,
-                               accum=TE_ACCUM_FULL_FP32)
-        wbuf, fused = _grad_buffer(weight)
-        db = None
-        if ctx.has_bias:
-            db = torch.empty((weight.shape[0],), dtype=torch.float32, device=dy.device)
-            te_fp8_wgrad_accum_bgrad(qdyt, sdyt, BWD_DTYPE, qxt, sxt, FWD_DTYPE, wbuf, db, TE_ACCUM_FULL_FP32)
-        else:
-            te_fp8_wgrad_accum(qdyt, sdyt, BWD_DTYPE, qxt, sxt, FWD_DTYPE, wbuf, TE_ACCUM_FULL_FP32)
+        # What is frozen gets no product, and nothing added to its main_grad.
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        dx = dw = db = None
+        if need_x:
+            _, _, qwt, swt = ctx.cache.get(weight)
+            dx = te_fp8_gemm_dgrad(qdy, sdy, BWD_DTYPE, qwt, swt, FWD_DTYPE, dx_dtype=TE_DTYPE_BF16,
+                                   accum=TE_ACCUM_FULL_FP32)
+        if need_w or (ctx.has_bias and need_b):
+            wbuf, fused = _grad_buffer(weight) if need_w else (_unread(weight), True)
+            if ctx.has_bias:
+                db = torch.empty((weight.shape[0],), dtype=torch.float32, device=dy.device)
+                te_fp8_wgrad_accum_bgrad(qdyt, sdyt, BWD_DTYPE, qxt, sxt, FWD_DTYPE, wbuf, db, TE_ACCUM_FULL_FP32)
+            else:
+                te_fp8_wgrad_accum(qdyt, sdyt, BWD_DTYPE, qxt, sxt, FWD_DTYPE, wbuf, TE_ACCUM_FULL_FP32)
+            # (autograd wants the parameters' own dtype; with main_grad the fp32 sum stays there)
+            dw = None if fused else wbuf.to(weight.dtype)
         if ctx.keep is not None:
             ctx.keep.update(qdy=qdy, sdy=sdy, qdyt=qdyt, sdyt=sdyt, db32=db)
-        # (autograd wants the parameters' own dtype; with main_grad the fp32 sum stays there)
-        dw = None if fused else wbuf.to(weight.dtype)
-        return dx, dw, (db.to(torch.bfloat16) if db is not None else None), None, None, None
+        return dx, dw, (db.to(torch.bfloat16) if db is not None and need_b else None), None, None, None
 
 
 class _Fp8MlpFn(torch.autograd.Function):
@@ -167,29 +176,39 @@ class _Fp8MlpFn(torch.autograd.Function):
         qxt, sxt, z1, qht, sht, w1, w2 = ctx.saved_tensors
         dy = dy.contiguous()
         qdy, sdy, qdyt, sdyt = te_cast_fp8_per_token_transpose(dy, BWD_DTYPE)
+        # What is frozen gets no product, and nothing added to its main_grad.
+        need_x, need_w1, need_b1, need_w2, need_b2 = ctx.needs_input_grad[:5]
+        dx = dw1 = db1 = dw2 = db2 = dz1 = qdz = sdz = qdzt = sdzt = None
         # fc2: weight gradient with its bias gradient; data gradient through fc1's GELU with fc1's bias gradient
-        w2buf, f2 = _grad_buffer(w2)
-        db2 = torch.empty((w2.shape[0],), dtype=torch.float32, device=dy.device)
-        te_fp8_wgrad_accum_bgrad(qdyt, sdyt, BWD_DTYPE, qht, sht, FWD_DTYPE, w2buf, db2, TE_ACCUM_FULL_FP32)
-        _, _, qw2t, sw2t = ctx.c2.get(w2)
-        # (fc1's bias gradient summed in a fixed order: reproducible from run to run, at the atomic
-        # form's speed -- the MLP step measured 3339 us atomic, 3345 us ordered)
-        db1 = torch.empty((w1.shape[0],), dtype=torch.float32, device=dy.device)
-        dz1 = te_fp8_gemm_dgrad_deterministic(qdy, sdy, BWD_DTYPE, qw2t, sw2t, FWD_DTYPE, db1,
-                                              epilogue=TE_EPI_DGELU | TE_EPI_BGRAD, preact=z1,
-                                              dx_dtype=TE_DTYPE_BF16, accum=TE_ACCUM_FULL_FP32)
+        if need_w2 or need_b2:
+            w2buf, f2 = _grad_buffer(w2) if need_w2 else (_unread(w2), True)
+            db2 = torch.empty((w2.shape[0],), dtype=torch.float32, device=dy.device)
+            te_fp8_wgrad_accum_bgrad(qdyt, sdyt, BWD_DTYPE, qht, sht, FWD_DTYPE, w2buf, db2, TE_ACCUM_FULL_FP32)
+            dw2 = None if f2 else w2buf.to(w2.dtype)
+        if need_x or need_w1 or need_b1:
+            _, _, qw2t, sw2t = ctx.c2.get(w2)
+            # (fc1's bias gradient summed in a fixed order: reproducible from run to run, at the atomic
+            # form's speed -- the MLP step measured 3339 us atomic, 3345 us ordered)
+            db1 = torch.empty((w1.shape[0],), dtype=torch.float32, device=dy.device)
+            dz1 = te_fp8_gemm_dgrad_deterministic(qdy, sdy, BWD_DTYPE, qw2t, sw2t, FWD_DTYPE, db1,
+                                                  epilogue=TE_EPI_DGELU | TE_EPI_BGRAD, preact=z1,
+                                                  dx_dtype=TE_DTYPE_BF16, accum=TE_ACCUM_FULL_FP32)
         # fc1
-        qdz, sdz, qdzt, sdzt = te_cast_fp8_per_token_transpose(dz1, BWD_DTYPE)
-        w1buf, f1 = _grad_buffer(w1)
-        te_fp8_wgrad_accum(qdzt, sdzt, BWD_DTYPE, qxt, sxt, FWD_DTYPE, w1buf, TE_ACCUM_FULL_FP32)
-        _, _, qw1t, sw1t = ctx.c1.get(w1)
-        dx = te_fp8_gemm_dgrad(qdz, sdz, BWD_DTYPE, qw1t, sw1t, FWD_DTYPE, dx_dtype=TE_DTYPE_BF16,
-                               accum=TE_ACCUM_FULL_FP32)
+        if need_x or need_w1:
+            qdz, sdz, qdzt, sdzt = te_cast_fp8_per_token_transpose(dz1, BWD_DTYPE)
+        if need_w1:
+            w1buf, f1 = _grad_buffer(w1)
+            te_fp8_wgrad_accum(qdzt, sdzt, BWD_DTYPE, qxt, sxt, FWD_DTYPE, w1buf, TE_ACCUM_FULL_FP32)
+            dw1 = None if f1 else w1buf.to(w1.dtype)
+        if need_x:
+            _, _, qw1t, sw1t = ctx.c1.get(w1)
+            dx = te_fp8_gemm_dgrad(qdz, sdz, BWD_DTYPE, qw1t, sw1t, FWD_DTYPE, dx_dtype=TE_DTYPE_BF16,
+                                   accum=TE_ACCUM_FULL_FP32)
         if ctx.keep is not None:
             ctx.keep.update(qdy=qdy, sdy=sdy, qdyt=qdyt, sdyt=sdyt, dz1=dz1, db1_32=db1, db2_32=db2, qdz=qdz,
                             sdz=sdz, qdzt=qdzt, sdzt=sdzt)
-        return (dx, None if f1 else w1buf.to(w1.dtype), db1.to(torch.bfloat16), None if f2 else w2buf.to(w2.dtype),
-                db2.to(torch.bfloat16), None, None, None, None)
+        return (dx, dw1, db1.to(torch.bfloat16) if need_b1 else None, dw2, db2.to(torch.bfloat16) if need_b2 else None,
+                None, None, None, None)
 
 
 def _init_weight(out_f, in_f, device, gen):

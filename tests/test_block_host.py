@@ -230,3 +230,55 @@ def test_clip_takes_one_parameter_for_a_list(calls):
     a = torch.nn.Parameter(torch.zeros(4, 4, dtype=torch.bfloat16))
     a.main_grad = torch.full((4, 4), 2.0)
     assert float(block.clip_grad_norm(a, 4.0)) == 8.0 and torch.allclose(a.main_grad, torch.ones(4, 4))
+
+
+# ------------------------------------------------------------------ linear.py
+@pytest.mark.parametrize("main_grad", [False, True])
+@pytest.mark.parametrize("train", ["x", "w", "b", "xw", "xb", "wb", "xwb"])
+def test_linear_with_frozen_parameters(calls, train, main_grad):
+    m = linear.Fp8Linear(128, 256, device="cpu", generator=torch.Generator().manual_seed(0), fuse_wgrad_accumulation=main_grad)
+    m.weight.requires_grad_("w" in train)
+    m.bias.requires_grad_("b" in train)
+    x = randn((128, 128), 1).requires_grad_("x" in train)
+    y = m(x)
+    dy = randn(y.shape, 2, 0.1)
+    y.backward(dy)
+    assert ("x" in train) == (x.grad is not None)
+    if "x" in train:
+        assert close(x.grad, dy.float() @ m.weight.detach().float())
+    if "w" in train:
+        assert close(got(m.weight), dy.float().t() @ x.detach().float())
+    else:
+        assert m.weight.grad is None and bool((getattr(m.weight, "main_grad", torch.zeros(1)) == 0).all())
+    assert close(m.bias.grad, dy.float().sum(0)) if "b" in train else m.bias.grad is None
+    assert calls.log.count("wgrad") == ("w" in train or "b" in train) and calls.log.count("dgrad") == ("x" in train)
+
+
+@pytest.mark.parametrize("main_grad", [False, True])
+@pytest.mark.parametrize("frozen", [(), ("w1",), ("w2",), ("w1", "w2"), ("b1", "b2"), ("w1", "b1"), ("w2", "b2"),
+                                    ("w1", "b1", "w2", "b2"), ("w1", "b1", "b2"), ("b1", "w2", "b2")], ids="+".join)
+@pytest.mark.parametrize("inputs", [True, False])
+def test_mlp_with_frozen_parameters(calls, frozen, inputs, main_grad):
+    names = ("w1", "b1", "w2", "b2")
+    if not inputs and set(frozen) == set(names):
+        pytest.skip("nothing takes a gradient")
+    m = linear.Fp8Mlp(128, 256, 128, device="cpu", generator=torch.Generator().manual_seed(0), fuse_wgrad_accumulation=main_grad)
+    m.b1.data.copy_(randn((256,), 5, 0.1))
+    for n in frozen:
+        m.get_parameter(n).requires_grad_(False)
+    x = randn((128, 128), 1).requires_grad_(inputs)
+    y = m(x)
+    dy = randn(y.shape, 3, 0.1)
+    leaves = [t.detach().float().requires_grad_() for t in (x, m.w1, m.b1, m.w2, m.b2)]
+    x32, w1, b1, w2, b2 = leaves
+    (torch.nn.functional.gelu(x32 @ w1.t() + b1, approximate="tanh") @ w2.t() + b2).backward(dy.float())
+    del calls.log[:]
+    y.backward(dy)
+    assert not inputs or close(x.grad, x32.grad)
+    for n, w in zip(names, leaves[1:]):
+        p = m.get_parameter(n)
+        if n in frozen:
+            assert p.grad is None and bool((getattr(p, "main_grad", torch.zeros(1)) == 0).all()), n
+        else:
+            assert close(got(p), w.grad), n
+    assert calls.log.count("wgrad") == ("w1" not in frozen) + (not {"w2", "b2"} <= set(frozen))
