@@ -17,7 +17,7 @@ from . import (TE_ACCUM_FULL_FP32, TE_DTYPE_BF16, TE_EPI_AUX_PREACT, TE_EPI_BGRA
                te_cast_fp8_per_token_transpose, te_fp8_gemm_dgrad, te_fp8_gemm_dgrad_deterministic, te_fp8_gemm_fwd,
                te_fp8_wgrad_accum, te_fp8_wgrad_accum_bgrad, te_grad_norm_clip, te_moe_router_bwd, te_moe_router_fwd,
                te_rmsnorm_bwd, te_rmsnorm_fwd)
-from .linear import BWD_DTYPE, FWD_DTYPE, Fp8Mlp, _check_dims, _fwd_policy, _grad_buffer, _unread
+from .linear import BWD_DTYPE, FWD_DTYPE, Fp8Mlp, _check_dims, _first_order, _fwd_policy, _grad_buffer, _unread
 
 
 def _to_param(grad32, param):
@@ -41,9 +41,14 @@ class _RmsNormFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy, dh_next):
-        h, rstd, gamma = ctx.saved_tensors
         if dy is None:      # only h was used
             return (dh_next.to(ctx.x_dtype) if dh_next is not None else None), dh_next, None, None
+        return _RmsNormFn.gradients(ctx, dy, dh_next)
+
+    @staticmethod
+    @_first_order
+    def gradients(ctx, dy, dh_next):
+        h, rstd, gamma = ctx.saved_tensors
         train = ctx.needs_input_grad[2]      # a frozen weight: no sums, and nothing added to its main_grad
         dh, dgamma = te_rmsnorm_bwd(dy.contiguous(), h, rstd, gamma, dres=dh_next.contiguous() if dh_next is not None else None,
                                     need_dgamma=train)
@@ -91,15 +96,21 @@ class _Fp8NormMlpFn(torch.autograd.Function):
         qw2, sw2, _, _ = c2.get(w2)
         y = te_fp8_gemm_fwd(qa, sa, FWD_DTYPE, qw2, sw2, FWD_DTYPE, bias=b2, epilogue=TE_EPI_BIAS, y_dtype=TE_DTYPE_BF16,
                             accum=accum)
-        ctx.save_for_backward(h, n.rstd, gamma, n.qt, n.scales_t, z1, qat, sat, w1, w2)
+        mark = x.new_empty(0)    # (as in linear's functions)
+        ctx.save_for_backward(h, n.rstd, gamma, n.qt, n.scales_t, z1, qat, sat, w1, w2, mark)
         ctx.c1, ctx.c2, ctx.added, ctx.x_dtype = c1, c2, residual is not None, x.dtype
-        return (y, h) if residual is not None else (y, None)
+        return y, (h if residual is not None else None), mark
 
     @staticmethod
-    def backward(ctx, dy, dh_next):
-        h, rstd, gamma, qnt, snt, z1, qat, sat, w1, w2 = ctx.saved_tensors
+    def backward(ctx, dy, dh_next, _):
         if dy is None:      # only h was used
             return (dh_next.to(ctx.x_dtype) if dh_next is not None else None), dh_next, *[None] * 9
+        return _Fp8NormMlpFn.gradients(ctx, dy, dh_next)
+
+    @staticmethod
+    @_first_order
+    def gradients(ctx, dy, dh_next):
+        h, rstd, gamma, qnt, snt, z1, qat, sat, w1, w2, _ = ctx.saved_tensors
         # What is frozen gets no product, no sum, and nothing added to its main_grad.
         need_x, need_res, need_gamma, _, need_w1, need_b1, need_w2, need_b2 = ctx.needs_input_grad[:8]
         through = need_x or need_res or need_gamma      # the gradient goes on below fc1
@@ -148,8 +159,8 @@ class Fp8NormMlp(torch.nn.Module):
     def forward(self, x, residual=None):
         shp, m = x.shape, self.mlp
         flat = residual.reshape(-1, shp[-1]) if residual is not None else None
-        y, h = _Fp8NormMlpFn.apply(x.reshape(-1, shp[-1]), flat, self.norm.weight, self.norm.eps, m.w1, m.b1, m.w2, m.b2, m.c1,
-                                   m.c2, m.pow2_scales)
+        y, h, _ = _Fp8NormMlpFn.apply(x.reshape(-1, shp[-1]), flat, self.norm.weight, self.norm.eps, m.w1, m.b1, m.w2, m.b2,
+                                      m.c1, m.c2, m.pow2_scales)
         return y.reshape(*shp[:-1], y.shape[-1]), (x if h is None else h.reshape(shp))
 
 
@@ -164,6 +175,7 @@ class _RouterFn(torch.autograd.Function):
         return r.weight, r.loss, r.index, r.counts
 
     @staticmethod
+    @_first_order
     def backward(ctx, d_weight, d_loss, _index, _counts):
         logits, index, lse, counts, routed = ctx.saved_tensors
         d = te_moe_router_bwd(logits, index, lse, counts, routed, renormalize=ctx.renormalize,

@@ -35,6 +35,7 @@ both the token and the feature dimensions).  Weights and activations are bf16.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -104,6 +105,38 @@ def _unread(weight: torch.Tensor):
     return torch.empty(weight.shape, dtype=torch.float32, device=weight.device)
 
 
+class _Refuse(torch.autograd.Function):
+    """Hands gradients on; who goes back through it asks for a derivative that does not exist."""
+
+    @staticmethod
+    def forward(ctx, name: str, count: int, *tensors):
+        ctx.name = name
+        return tuple(t.detach() for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name}: its second derivative is not implemented")
+
+
+def _first_order(backward):
+    """For a backward pass made of library calls, which autograd does not see: with create_graph=True its gradients
+    would come back as constants, and whatever is built on them would lose its own gradient without an error.
+    They are tied to all that they depend on instead (the incoming gradients and the saved tensors, among which are
+    the function's inputs or one of its outputs), and differentiating them again raises."""
+    @functools.wraps(backward)
+    def run(ctx, *incoming):
+        if not torch.is_grad_enabled():     # (no create_graph)
+            return backward(ctx, *incoming)
+        with torch.no_grad():
+            grads = list(backward(ctx, *incoming))
+        at = [i for i, g in enumerate(grads) if g is not None]
+        tied = [t for t in (*incoming, *ctx.saved_tensors) if t is not None and t.requires_grad]
+        for i, g in zip(at, _Refuse.apply(backward.__qualname__.split(".")[0].strip("_"), len(at), *[grads[i] for i in at], *tied)):
+            grads[i] = g
+        return tuple(grads)
+    return run
+
+
 class _Fp8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, cache: Fp8WeightCache, keep: dict | None, pow2: bool):
@@ -116,15 +149,18 @@ class _Fp8LinearFn(torch.autograd.Function):
         y = te_fp8_gemm_fwd(qx, sx, FWD_DTYPE, qw, sw, FWD_DTYPE, bias=bias,
                             epilogue=TE_EPI_BIAS if bias is not None else TE_EPI_NONE, y_dtype=TE_DTYPE_BF16,
                             accum=accum)
-        ctx.save_for_backward(qxt, sxt, weight)
+        mark = x.new_empty(0)    # an output that is saved, for _first_order: x itself is not
+        ctx.save_for_backward(qxt, sxt, weight, mark)
+        ctx.set_materialize_grads(False)
         ctx.cache, ctx.has_bias, ctx.keep = cache, bias is not None, keep
         if keep is not None:
             keep.update(qx=qx, sx=sx, qxt=qxt, sxt=sxt)
-        return y
+        return y, mark
 
     @staticmethod
-    def backward(ctx, dy):
-        qxt, sxt, weight = ctx.saved_tensors
+    @_first_order
+    def backward(ctx, dy, _):
+        qxt, sxt, weight, _ = ctx.saved_tensors
         dy = dy.contiguous()
         qdy, sdy, qdyt, sdyt = te_cast_fp8_per_token_transpose(dy, BWD_DTYPE)
         # What is frozen gets no product, and nothing added to its main_grad.
@@ -165,15 +201,18 @@ class _Fp8MlpFn(torch.autograd.Function):
         qw2, sw2, _, _ = c2.get(w2)
         y = te_fp8_gemm_fwd(qh, sh, FWD_DTYPE, qw2, sw2, FWD_DTYPE, bias=b2, epilogue=TE_EPI_BIAS,
                             y_dtype=TE_DTYPE_BF16, accum=accum)
-        ctx.save_for_backward(qxt, sxt, z1, qht, sht, w1, w2)
+        mark = x.new_empty(0)    # (as in _Fp8LinearFn)
+        ctx.save_for_backward(qxt, sxt, z1, qht, sht, w1, w2, mark)
+        ctx.set_materialize_grads(False)
         ctx.c1, ctx.c2, ctx.keep = c1, c2, keep
         if keep is not None:
             keep.update(qx=qx, sx=sx, qxt=qxt, sxt=sxt, z1=z1, h=h, qh=qh, sh=sh, qht=qht, sht=sht)
-        return y
+        return y, mark
 
     @staticmethod
-    def backward(ctx, dy):
-        qxt, sxt, z1, qht, sht, w1, w2 = ctx.saved_tensors
+    @_first_order
+    def backward(ctx, dy, _):
+        qxt, sxt, z1, qht, sht, w1, w2, _ = ctx.saved_tensors
         dy = dy.contiguous()
         qdy, sdy, qdyt, sdyt = te_cast_fp8_per_token_transpose(dy, BWD_DTYPE)
         # What is frozen gets no product, and nothing added to its main_grad.
@@ -240,8 +279,8 @@ class Fp8Linear(torch.nn.Module):
 
     def forward(self, x):
         shp = x.shape
-        y = _Fp8LinearFn.apply(x.reshape(-1, shp[-1]), self.weight, self.bias, self.cache, self.keep,
-                               self.pow2_scales)
+        y, _ = _Fp8LinearFn.apply(x.reshape(-1, shp[-1]), self.weight, self.bias, self.cache, self.keep,
+                                  self.pow2_scales)
         return y.reshape(*shp[:-1], y.shape[-1])
 
 
@@ -268,6 +307,6 @@ class Fp8Mlp(torch.nn.Module):
 
     def forward(self, x):
         shp = x.shape
-        y = _Fp8MlpFn.apply(x.reshape(-1, shp[-1]), self.w1, self.b1, self.w2, self.b2, self.c1, self.c2, self.keep,
-                            self.pow2_scales)
+        y, _ = _Fp8MlpFn.apply(x.reshape(-1, shp[-1]), self.w1, self.b1, self.w2, self.b2, self.c1, self.c2, self.keep,
+                               self.pow2_scales)
         return y.reshape(*shp[:-1], y.shape[-1])

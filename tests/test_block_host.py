@@ -282,3 +282,84 @@ def test_mlp_with_frozen_parameters(calls, frozen, inputs, main_grad):
         else:
             assert close(got(p), w.grad), n
     assert calls.log.count("wgrad") == ("w1" not in frozen) + (not {"w2", "b2"} <= set(frozen))
+
+
+# ------------------------------------------------------------------ second derivatives
+def first_gradients(make, inputs, params):
+    """The module's outputs that take a gradient, and their gradients with the graph kept."""
+    outs = [o for o in make(*inputs) if o is not None and o.requires_grad and o.is_floating_point() and o.numel()]
+    leaves = [t for t in (*inputs, *params) if t is not None and t.requires_grad]
+    value = sum((o.float() * randn(o.shape, 9 + i, dtype=torch.float32)).sum() for i, o in enumerate(outs))
+    return leaves, torch.autograd.grad(value, leaves, create_graph=True, allow_unused=True)
+
+
+def second_order_cases():
+    def norm(residual, train=True):
+        m = block.RmsNorm(64, device="cpu", main_grad=False)
+        m.weight.requires_grad_(train)
+        res = randn((6, 64), 2).requires_grad_() if residual else None
+        return m, (randn((6, 64), 1).requires_grad_(), res), (m.weight,)
+
+    def mlp(cls, frozen=()):
+        m = cls(128, 256, 128, device="cpu", generator=torch.Generator().manual_seed(0))
+        for n, p in m.named_parameters():
+            p.requires_grad_(n not in frozen)
+            if hasattr(p, "main_grad"):
+                del p.main_grad
+        run = m if cls is block.Fp8NormMlp else lambda x: (m(x),)
+        return run, (randn((128, 128), 1).requires_grad_(),), tuple(m.parameters())
+
+    def linear_(train):
+        m = linear.Fp8Linear(128, 256, device="cpu", generator=torch.Generator().manual_seed(0), fuse_wgrad_accumulation=False)
+        m.weight.requires_grad_(train)
+        return lambda x: (m(x),), (randn((128, 128), 1).requires_grad_(),), (m.weight, m.bias)
+
+    def router(renormalize):
+        m = block.TopKRouter(2, renormalize)
+        return lambda v: m(v)[:2], (randn((6, 8), 1, dtype=torch.float32).requires_grad_(),), ()
+
+    mlp_names, weights = ("w1", "b1", "w2", "b2"), ("norm.weight", "mlp.w1", "mlp.w2")
+    return dict(norm=lambda: norm(False), norm_residual=lambda: norm(True), norm_frozen=lambda: norm(False, False),
+                norm_mlp=lambda: mlp(block.Fp8NormMlp), norm_mlp_frozen=lambda: mlp(block.Fp8NormMlp, weights),
+                mlp=lambda: mlp(linear.Fp8Mlp), mlp_frozen=lambda: mlp(linear.Fp8Mlp, mlp_names),
+                linear=lambda: linear_(True), linear_frozen=lambda: linear_(False), router=lambda: router(False))
+
+
+@pytest.mark.parametrize("case", list(second_order_cases()))
+def test_second_derivatives_are_refused(calls, case):
+    """Any value made of the first gradients: differentiated for the inputs, or for any parameter, it raises; the
+    first gradients themselves are those without create_graph."""
+    make, inputs, params = second_order_cases()[case]()
+    leaves, first = first_gradients(make, inputs, params)
+    plain = torch.autograd.grad(sum((o.float() * randn(o.shape, 9 + i, dtype=torch.float32)).sum() for i, o in enumerate(
+        [o for o in make(*inputs) if o is not None and o.requires_grad and o.is_floating_point() and o.numel()])), leaves, allow_unused=True)
+    assert all((a is None) == (b is None) and (a is None or torch.equal(a, b)) for a, b in zip(first, plain))
+    for g in first:
+        penalty = g.float().square().sum()
+        for leaf in leaves:
+            with pytest.raises(RuntimeError, match="second derivative"):
+                torch.autograd.grad(penalty, [leaf], retain_graph=True, allow_unused=True)
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (penalty + sum(t.float().sum() for t in leaves)).backward(retain_graph=True)
+
+
+def test_first_derivatives_beside_a_second_one_elsewhere(calls):
+    """create_graph=True for the sake of another part of the model: the modules' own gradients stay usable."""
+    m = block.RmsNorm(64, device="cpu", main_grad=False)
+    x = randn((6, 64), 1, dtype=torch.float32).requires_grad_()
+    a = randn((64,), 2, dtype=torch.float32).requires_grad_()
+    y, _ = m(x)
+    value = (y.float() * 2).sum() + (a ** 3).sum()
+    gx, ga = torch.autograd.grad(value, [x, a], create_graph=True)
+    assert torch.equal(torch.autograd.grad(ga.sum(), a)[0], 6 * a.detach()) and bool((gx != 0).any())
+
+
+@pytest.mark.parametrize("cls", ["norm", "mlp"])
+def test_the_sum_alone_can_be_differentiated_again(calls, cls):
+    """h = x + residual is an addition: where only it is used, its gradient is handed on with its graph."""
+    m = norm_mlp() if cls == "mlp" else block.RmsNorm(128, device="cpu")
+    x, res = (randn((128, 128), i, dtype=torch.float32).requires_grad_() for i in (1, 2))
+    _, h = m(x, res)
+    g, = torch.autograd.grad((h ** 3).sum(), x, create_graph=True)
+    again, = torch.autograd.grad(g.sum(), res)
+    assert torch.allclose(again, 6 * h.detach())
