@@ -101,11 +101,19 @@ __device__ __forceinline__ float row_sum(float v, float* red)
     return s;
 }
 
+// The largest |y|, NaN if one is NaN: a group with what is not finite is to stand for NaN, and codes
+// alone cannot say so (they saturate, and e4m3 has no infinity), so its scale does.
+__device__ __forceinline__ float amax_keep(float amax, float y) { return __builtin_elementwise_maximum(amax, fabsf(y)); }
+// (the bits of numbers without a sign are in the numbers' order, and NaN's are above all)
+template <int kLanes>
+__device__ __forceinline__ float amax_lanes(float amax) { return as_float(max_lanes<kLanes>(as_bits(amax))); }
+
 template <int kFmt, bool kPow2>
 __device__ __forceinline__ uint2 cast8(const float (&y)[8], float amax, float& scale)
 {
     float mult, s[8];
     group_scale<kFmt, kPow2>(amax, scale, mult);
+    if (!(amax < __builtin_inff())) scale = __builtin_nanf("");
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = y[j] * mult;
     return encode8<kFmt>(s);
@@ -184,8 +192,8 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void rmsnorm_fwd_kernel(const Nor
         else if (a.y) {   // fp8: cols is a multiple of 128, a group is sixteen lanes wide
             float amax = 0.0f, scale;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
-            amax = max_lanes<16>(amax);
+            for (int j = 0; j < 8; ++j) amax = amax_keep(amax, y[j]);
+            amax = amax_lanes<16>(amax);
             const uint2 q = cast8(a.fmt, a.pow2, y, amax, scale);
             if (c[i].on) {
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + row * a.ld_y + c[i].c0) = q;
@@ -268,12 +276,12 @@ void rmsnorm_cast_transpose_kernel(const NormFwdArgs a)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             y[q][k >> 3][k & 7] = v[q] * rs[k] * g[q];
-            amax[q] = fmaxf(amax[q], fabsf(y[q][k >> 3][k & 7]));
+            amax[q] = amax_keep(amax[q], y[q][k >> 3][k & 7]);
         }
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        amax[q] = max_lanes<8>(amax[q]);
+        amax[q] = amax_lanes<8>(amax[q]);
         float scale;
         const uint2 e0 = cast8<kFmt, kPow2>(y[q][0], amax[q], scale);
         const uint2 e1 = cast8<kFmt, kPow2>(y[q][1], amax[q], scale);

@@ -199,14 +199,14 @@ __device__ __forceinline__ float sum_lanes(float v)
     return v;
 }
 template <int kLanes>
-__device__ __forceinline__ float max_lanes(float v)
+__device__ __forceinline__ uint32_t max_lanes(uint32_t v)
 {
-    if (kLanes > 1) v = fmaxf(v, partner<1>(v));
-    if (kLanes > 2) v = fmaxf(v, partner<2>(v));
-    if (kLanes > 4) v = fmaxf(v, partner<4>(v));
-    if (kLanes > 8) v = fmaxf(v, partner<8>(v));
-    if (kLanes > 16) v = fmaxf(v, partner<16>(v));
-    if (kLanes > 32) v = fmaxf(v, partner<32>(v));
+    if (kLanes > 1) v = max(v, (uint32_t)partner<1>((int)v));
+    if (kLanes > 2) v = max(v, (uint32_t)partner<2>((int)v));
+    if (kLanes > 4) v = max(v, (uint32_t)partner<4>((int)v));
+    if (kLanes > 8) v = max(v, (uint32_t)partner<8>((int)v));
+    if (kLanes > 16) v = max(v, (uint32_t)partner<16>((int)v));
+    if (kLanes > 32) v = max(v, (uint32_t)partner<32>((int)v));
     return v;
 }
 

@@ -43,6 +43,9 @@ extern "C" {
  *       and / or as the cast of its transpose (groups of 128 rows, rows a
  *       multiple of 128, cols a multiple of 8) in qt [cols][ld_qt] and scales_t
  *       [rows/128][te_scale_ld(cols)].  Either pair may be null, not both.
+ *       Non-finite values: where a group of either cast holds a y that is NaN
+ *       or infinite, its scale is NaN, so all that the group stands for is (its
+ *       codes are unspecified).
  *
  *  x, residual   TE_DTYPE_BF16 or TE_DTYPE_F32, each on its own
  *  gamma         [cols] bf16
