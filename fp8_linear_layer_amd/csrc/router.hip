@@ -52,18 +52,36 @@ __device__ __forceinline__ float from_order_key(int32_t k)
 // The middle one; written so that it becomes one instruction.
 __device__ __forceinline__ int32_t med3(int32_t a, int32_t b, int32_t x) { return max(min(a, b), min(max(a, b), x)); }
 
-// exp for arguments at or below zero: one product and the hardware's exp2, off by about |x| 2^-24 of
-// the value, which the sums and the bf16 results here do not feel (a term that is far down weighs little) ...
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
-// ... and with the product's rounding, and log2(e)'s, carried along, for the fp32 results.  (The
-// bound keeps the correction finite where the result is zero; it drops a NaN.)
+// exp for arguments at or below zero.  t = x log2(e) is rounded, which would be |x| 2^-24 of the result; what it is
+// off by, x - t ln 2, comes back as a factor.  The constant is the float above log2(e), so that this is never
+// negative (at most |x| 2^-22), and its bounds 0 and 1 cost nothing (the instruction clamps) and make a zero of the
+// NaN at x = -inf; a NaN x stays NaN by t.  ln 2 as a float adds |x| 2^-28.
 __device__ __forceinline__ float exp_exact(float x)
 {
-    x = fmaxf(x, -1e30f);
-    const float t = x * 1.44269504f;
-    const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));
+    float ln2 = -0.693147182f;
+    asm("" : "+s"(ln2));   // (in a register: an instruction with a literal has no clamp)
+    const float t = x * 1.44269514f;
+    const float r = __builtin_amdgcn_fmed3f(fmaf(t, ln2, x), 0.0f, 1.0f);
     const float e = __builtin_amdgcn_exp2f(t);
-    return fmaf(e, r * 0.693147181f, e);
+    return fmaf(e, r, e);
+}
+// The product alone, for what is stored in bf16 next: off by |x| 2^-24 of the result, where the store rounds by
+// 2^-8 (the backward pass in bf16: 13.6 us so, 14.3 with exp_exact).
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// A sum in pairs: one after the other, equal small terms on top of a large one are all rounded the same way (2047
+// logits 7.6 below the largest: the row's sum off by 6 steps of 2^-24 rms that way, by 1 in pairs).
+template <int kN> __device__ __forceinline__ float sum_pairs(const float (&v)[kN])
+{
+    static_assert((kN & (kN - 1)) == 0, "halves");
+    float s[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) s[i] = v[i];
+#pragma unroll
+    for (int n = kN / 2; n >= 1; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i) s[i] += s[i + n];
+    return s[0];
 }
 
 // A sorted list of the kK largest (key, column), equal keys by the lower column.
@@ -279,7 +297,7 @@ constexpr int kFwdThreads = 512;
 constexpr int kFwdWaves = kFwdThreads / 64;
 
 // (Waves per SIMD that the registers are cut for: four take 128 each, which the long lists and the rows of
-// fp32 do not fit.)
+// fp32 do not fit, and the lists of 4 and 8 on 32 lanes but for one register, which is spilled.)
 template <class T, int kNC, int kK> constexpr int kFwdWavesPerSimd = kK == 16 || (kNC == 4 && __is_same(T, F32)) ? 2 : 4;
 
 template <class T, int kL, int kNC, int kK, bool kLoss>
@@ -351,19 +369,16 @@ __global__ __launch_bounds__(kFwdThreads, (kFwdWavesPerSimd<T, kNC, kK>)) void r
         if (__any(top.key(0) > kOpenInf)) select(true);
 
         const float m = top.key(0) > kClosed ? from_order_key(top.key(0)) : 0.0f;
-        float s = 0.0f;
-        float e[kNC][8];
+        float e[kNC][8], part[kNC];
 #pragma unroll
         for (int i = 0; i < kNC; ++i) {
             float v[8];
             unpack8(raw[i], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                e[i][j] = exp_fast(v[j] - m);
-                s += e[i][j];
-            }
+            for (int j = 0; j < 8; ++j) e[i][j] = exp_exact(v[j] - m);
+            part[i] = sum_pairs(e[i]);
         }
-        s = sum_lanes<kL>(s);
+        const float s = sum_lanes<kL>(sum_pairs(part));
         const bool sent = live && top.key(0) > kClosed;
 
         // lane p has entries p, p + kL, ...
@@ -384,10 +399,9 @@ __global__ __launch_bounds__(kFwdThreads, (kFwdWavesPerSimd<T, kNC, kK>)) void r
             if (!chosen) col[q] = -1;
             sum += ev[q];
         }
-        // (the hardware's reciprocal, one step of 2^-23 off at most: the sums are no better)
-        const float inv = __builtin_amdgcn_rcpf(s);
+        const float inv = 1.0f / s;
         float scale = inv;
-        if (a.renorm) scale = s == s ? __builtin_amdgcn_rcpf(sum_lanes<kL>(sum)) : s;
+        if (a.renorm) scale = s == s ? 1.0f / sum_lanes<kL>(sum) : s;
 #pragma unroll
         for (int q = 0; q < kOwn; ++q) {
             const int j = q * kL + p;
