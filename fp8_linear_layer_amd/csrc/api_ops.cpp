@@ -1,6 +1,7 @@
 // C-ABI front end of the operators around the GEMMs (te_ops.h): argument validation, dispatch,
 // per-call logging.  The rules are those of api.cpp: every check runs on the host before anything
 // is enqueued, nothing is allocated, nothing synchronises.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -349,7 +350,7 @@ te_status_t te_moe_router_bwd(const void* logits, te_dtype_t logits_dtype, int64
     }
 }
 
-int64_t te_grad_norm_workspace_bytes(int64_t n) { return n < 0 ? 0 : tefp8::clip_workspace_bytes(n); }
+int64_t te_grad_norm_workspace_bytes(int64_t n) { return n < 0 ? 0 : tefp8::clip_workspace_bytes(); }
 
 te_status_t te_grad_norm_clip(const te_grad_tensor_t* tensors, int64_t n, float max_norm, float* norm, void* workspace,
                               int64_t workspace_bytes, hipStream_t stream)
@@ -394,9 +395,9 @@ te_status_t te_grad_norm_clip(const te_grad_tensor_t* tensors, int64_t n, float 
         int64_t slots = 0, launches = 0;
         for (int64_t at = 0;;) {
             const int64_t next = fill(b, at);
-            const hipError_t e = tefp8::launch_grad_sumsq(b, partial + slots, stream);
+            const hipError_t e = tefp8::launch_grad_sumsq(b, partial, slots, stream);
             if (e != hipSuccess) return launched(fn, e);
-            slots += tefp8::clip_blocks(b);
+            slots = std::max(slots, tefp8::clip_blocks(b));
             ++launches;
             if (next >= n) break;
             at = next;

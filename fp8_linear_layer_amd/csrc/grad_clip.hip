@@ -5,9 +5,10 @@
 // Memory-bound: the gradients are read twice (the coefficient depends on all of them) and the
 // outputs written once.  The tensors are cut into chunks of kChunk elements, which the workgroups
 // take in turn; the tensors' addresses travel in the kernel's arguments, so nothing is copied to the
-// device first.  The first kernel leaves one sum of squares per workgroup, in fp64 (a square of an
-// fp32 gradient need not fit fp32's range); in the second every workgroup adds those up in the same
-// fixed order, which costs less than a launch between the two.  The second goes through the chunks
+// device first; one launch takes kClipBatch of them.  The first kernel leaves one sum of squares per
+// workgroup, in fp64 (a square of an fp32 gradient need not fit fp32's range); later launches add to the
+// sums of the earlier ones' workgroups, so that there are never more than kClipBlocks.  In the second kernel every
+// workgroup adds those up in the same fixed order, which costs less than a launch between the two.  The second goes through the chunks
 // backwards: what the first read last is what the caches still hold (with gradients many times their size
 // the order makes no difference).
 //
@@ -124,8 +125,9 @@ __device__ __forceinline__ double block_sum(double v)
     return s;
 }
 
+// `have` sums are there from earlier launches.
 template <bool kStream>
-__global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const ClipBatch b, double* __restrict__ partial)
+__global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const ClipBatch b, double* __restrict__ partial, int have)
 {
     double s = 0.0;
     auto add = [&](const auto& v, int64_t, int) {
@@ -140,7 +142,7 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const ClipBatch b,
         else each_unit<F32, kStream>(b.t[i], first, add);
     }
     s = block_sum(s);
-    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+    if (threadIdx.x == 0) partial[blockIdx.x] = (int)blockIdx.x < have ? partial[blockIdx.x] + s : s;
 }
 
 template <class G, class O, bool kStream>
@@ -209,16 +211,13 @@ int64_t clip_blocks(const ClipBatch& b) { return std::max(1, std::min(b.chunks, 
 
 int64_t clip_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 
-int64_t clip_workspace_bytes(int64_t tensors)
-{
-    return std::max<int64_t>(1, (tensors + kClipBatch - 1) / kClipBatch) * kClipBlocks * (int64_t)sizeof(double);
-}
+int64_t clip_workspace_bytes() { return kClipBlocks * (int64_t)sizeof(double); }
 
-hipError_t launch_grad_sumsq(const ClipBatch& b, double* partial, hipStream_t stream)
+hipError_t launch_grad_sumsq(const ClipBatch& b, double* partial, int64_t have, hipStream_t stream)
 {
     const unsigned grid = (unsigned)clip_blocks(b);
-    if (b.chunks >= kStreamChunks) grad_sumsq_kernel<true><<<grid, kThreads, 0, stream>>>(b, partial);
-    else grad_sumsq_kernel<false><<<grid, kThreads, 0, stream>>>(b, partial);
+    if (b.chunks >= kStreamChunks) grad_sumsq_kernel<true><<<grid, kThreads, 0, stream>>>(b, partial, (int)have);
+    else grad_sumsq_kernel<false><<<grid, kThreads, 0, stream>>>(b, partial, (int)have);
     return hipGetLastError();
 }
 

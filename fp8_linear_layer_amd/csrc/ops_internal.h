@@ -102,7 +102,7 @@ hipError_t launch_router_bwd(const RouterBwdArgs& a, hipStream_t stream);
 // ------------------------------------------------------------ gradient norm and clipping
 // Tensors of one launch: their descriptors travel in the kernel's arguments (at most 4 KiB).
 constexpr int kClipBatch = 96;
-constexpr int kClipBlocks = 1024;   // most workgroups of a launch; each has a slot for its sum
+constexpr int kClipBlocks = 1024;   // most workgroups of a launch; each has a slot for its sum, shared by the launches
 
 struct ClipTensor {
     const void* grad;
@@ -117,8 +117,8 @@ struct ClipBatch {
 };
 int64_t clip_chunks(int64_t n);
 int64_t clip_blocks(const ClipBatch& b);
-int64_t clip_workspace_bytes(int64_t tensors);
-hipError_t launch_grad_sumsq(const ClipBatch& b, double* partial, hipStream_t stream);
+int64_t clip_workspace_bytes();
+hipError_t launch_grad_sumsq(const ClipBatch& b, double* partial, int64_t have, hipStream_t stream);
 hipError_t launch_grad_scale(const ClipBatch& b, const double* partial, int64_t slots, float max_norm, float* norm,
                              hipStream_t stream);
 
