@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <vector>
 
 #include "internal.h"
 #include "ops_internal.h"
@@ -391,27 +392,31 @@ te_status_t te_grad_norm_clip(const te_grad_tensor_t* tensors, int64_t n, float 
             return at;
         };
         double* partial = static_cast<double*>(workspace);
+        int64_t bytes = 0;   // (of memory that exists: far below 2^63)
+        for (int64_t i = 0; i < n; ++i) bytes += tensors[i].count * size_of(tensors[i].grad_dtype);
+        const bool past = bytes >= tefp8::kClipPast;
         tefp8::ClipBatch b{};
-        int64_t slots = 0, launches = 0;
+        std::vector<int64_t> starts;
+        starts.reserve((size_t)(n / tefp8::kClipBatch + 1));
+        int64_t slots = 0;
         for (int64_t at = 0;;) {
+            starts.push_back(at);
             const int64_t next = fill(b, at);
-            const hipError_t e = tefp8::launch_grad_sumsq(b, partial, slots, stream);
+            const hipError_t e = tefp8::launch_grad_sumsq(b, partial, slots, past, stream);
             if (e != hipSuccess) return launched(fn, e);
             slots = std::max(slots, tefp8::clip_blocks(b));
-            ++launches;
             if (next >= n) break;
             at = next;
         }
-        for (int64_t at = 0;;) {
-            const int64_t next = fill(b, at);
-            const hipError_t e = tefp8::launch_grad_scale(b, partial, slots, max_norm, at == 0 ? norm : nullptr, stream);
+        const int64_t launches = (int64_t)starts.size();
+        for (int64_t i = launches - 1; i >= 0; --i) {
+            if (i < launches - 1) fill(b, starts[(size_t)i]);   // (the last one's is there)
+            const hipError_t e = tefp8::launch_grad_scale(b, partial, slots, max_norm, i == launches - 1 ? norm : nullptr, past, stream);
             if (e != hipSuccess) return launched(fn, e);
-            if (next >= n) break;
-            at = next;
         }
         if (tefp8::log_calls())
-            std::fprintf(stderr, "[te_fp8] %s n=%lld max_norm=%g batches=%lld slots=%lld\n", fn, (long long)n, (double)max_norm,
-                         (long long)launches, (long long)slots);
+            std::fprintf(stderr, "[te_fp8] %s n=%lld max_norm=%g batches=%lld slots=%lld past=%d\n", fn, (long long)n, (double)max_norm,
+                         (long long)launches, (long long)slots, past ? 1 : 0);
         return report_ok();
     } catch (...) {
         return report(TE_ERR_INTERNAL, "te_grad_norm_clip: internal error");

@@ -102,6 +102,11 @@ hipError_t launch_router_bwd(const RouterBwdArgs& a, hipStream_t stream);
 // ------------------------------------------------------------ gradient norm and clipping
 // Tensors of one launch: their descriptors travel in the kernel's arguments (at most 4 KiB).
 constexpr int kClipBatch = 96;
+// Gradients of this many bytes in a call go past the caches: twice the last cache's size.  Both passes, gradients just
+// written by another kernel, ordinarily and past the caches: fp32 into bf16 256 MiB 116.7 and 131.9 us, 512 MiB
+// 296.2 and 270.1; bf16 into bf16 256 MiB 150.4 and 167.1, 512 MiB 345.4 and 326.2 (bf16 into fp32, whose stores are
+// half lines, 498.3 and 516.6).  Gradients that nothing has touched gain 3 to 6 % from 256 MiB on.
+constexpr int64_t kClipPast = (int64_t)1 << 29;
 constexpr int kClipBlocks = 1024;   // most workgroups of a launch; each has a slot for its sum, shared by the launches
 
 struct ClipTensor {
@@ -118,8 +123,9 @@ struct ClipBatch {
 int64_t clip_chunks(int64_t n);
 int64_t clip_blocks(const ClipBatch& b);
 int64_t clip_workspace_bytes();
-hipError_t launch_grad_sumsq(const ClipBatch& b, double* partial, int64_t have, hipStream_t stream);
+// `have` sums are there from earlier launches; `past`: read and written past the caches.
+hipError_t launch_grad_sumsq(const ClipBatch& b, double* partial, int64_t have, bool past, hipStream_t stream);
 hipError_t launch_grad_scale(const ClipBatch& b, const double* partial, int64_t slots, float max_norm, float* norm,
-                             hipStream_t stream);
+                             bool past, hipStream_t stream);
 
 }  // namespace tefp8

@@ -13,6 +13,6 @@ hipError_t launch_router_bwd(const RouterBwdArgs&, hipStream_t) { return hipErro
 int64_t clip_chunks(int64_t n) { return (n + 8191) / 8192; }
 int64_t clip_blocks(const ClipBatch& b) { return b.chunks < 1 ? 1 : b.chunks < kClipBlocks ? b.chunks : kClipBlocks; }
 int64_t clip_workspace_bytes() { return kClipBlocks * 8; }
-hipError_t launch_grad_sumsq(const ClipBatch&, double*, int64_t, hipStream_t) { return hipErrorNoDevice; }
-hipError_t launch_grad_scale(const ClipBatch&, const double*, int64_t, float, float*, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_grad_sumsq(const ClipBatch&, double*, int64_t, bool, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_grad_scale(const ClipBatch&, const double*, int64_t, float, float*, bool, hipStream_t) { return hipErrorNoDevice; }
 }  // namespace tefp8

@@ -1,8 +1,12 @@
 """Host side of te_grad_norm_clip over long lists of tensors (CPU only)."""
+import ctypes
 import os
+import shutil
+import subprocess
 
 import pytest
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 te = pytest.importorskip("fp8_linear_layer_amd")
 from fp8_linear_layer_amd import ops  # noqa: E402
 
@@ -19,3 +23,64 @@ def test_partial_sums_do_not_grow_with_the_list(lib):
     that work grew with the square of the tensors."""
     sizes = {n: lib.te_grad_norm_workspace_bytes(n) for n in (0, 1, 96, 97, 1000, 18000, 1 << 20)}
     assert len(set(sizes.values())) == 1 and 0 < sizes[1] <= 8192, sizes
+
+
+class Launch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("which", "first_count", "tensors", "chunks", "slots", "past", "norm")]
+
+
+@pytest.fixture(scope="module")
+def recorder(tmp_path_factory):
+    """The front end with launchers that only note their arguments."""
+    if shutil.which("g++") is None:
+        pytest.skip("no host compiler")
+    out = str(tmp_path_factory.mktemp("clip") / "libte_fp8_record.so")
+    csrc, sub = os.path.join(ROOT, "fp8_linear_layer_amd", "csrc"), os.path.join(ROOT, "tests", "sanitize")
+    subprocess.run(["g++", "-std=c++17", "-fPIC", "-shared", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                    "-I", os.path.join(ROOT, "include"), "-I", csrc, os.path.join(csrc, "api.cpp"), os.path.join(csrc, "api_ops.cpp"),
+                    os.path.join(sub, "host_stubs.cpp"), os.path.join(sub, "host_record_clip.cpp"), "-o", out], check=True)
+    lib = ctypes.CDLL(out)
+    lib.recorded.restype = ctypes.c_int64
+    lib.te_grad_norm_clip.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_void_p]
+
+    def launches(counts, dtype=te.TE_DTYPE_F32):
+        arr = (ops._GradTensor * max(1, len(counts)))(*[(0x10000, 0x20000, n, dtype, te.TE_DTYPE_F32) for n in counts])
+        assert lib.te_grad_norm_clip(arr, len(counts), 1.0, 0x30000, 0x40000, 1 << 20, None) == 0
+        got = (Launch * 2000)()
+        return list(got[:lib.recorded(got, 2000)])
+    return launches
+
+
+def split(launches):
+    return [x for x in launches if x.which == 0], [x for x in launches if x.which == 1]
+
+
+@pytest.mark.parametrize("counts", [[], [0], [5], [100] * 96, [100] * 97, [100 + i for i in range(1000)], [10 ** 7] * 200, [0] * 200])
+def test_every_tensor_is_in_one_launch_of_each_pass(recorder, counts):
+    sums, scales = split(recorder(counts))
+    live = [n for n in counts if n]
+    for launches in (sums, scales):
+        assert sum(x.tensors for x in launches) == len(live) and sum(x.chunks for x in launches) == sum(-(-n // 8192) for n in live)
+    assert [x.norm for x in scales].count(1) == 1
+    blocks = [min(1024, max(1, x.chunks)) for x in sums]
+    assert [x.slots for x in sums] == [max(blocks[:i], default=0) for i in range(len(blocks))]
+    assert all(x.slots == max(blocks) for x in scales)
+
+
+def test_past_the_caches_goes_by_the_whole_list(recorder):
+    """Gradients of a gigabyte are far larger than the caches, in whatever number of tensors they come."""
+    mebi = 1 << 20
+    for counts in ([300 * mebi], [mebi] * 300, [mebi // 16] * 4800):
+        assert all(x.past for x in recorder(counts))
+        assert all(x.past for x in recorder(counts, te.TE_DTYPE_BF16))
+    for counts in ([16 * mebi], [mebi] * 16, [mebi // 16] * 256, [100] * 50000):
+        assert not any(x.past for x in recorder(counts))
+    assert all(x.past for x in recorder([150 * mebi])) and not any(x.past for x in recorder([150 * mebi], te.TE_DTYPE_BF16))
+
+
+def test_second_pass_starts_where_the_first_ended(recorder):
+    """Last launch first: what the first pass read last is what the caches still hold."""
+    sums, scales = split(recorder([1000 + i for i in range(500)]))
+    assert [x.first_count for x in scales] == [x.first_count for x in reversed(sums)]
+    assert len(sums) == 6
