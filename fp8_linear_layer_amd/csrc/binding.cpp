@@ -38,6 +38,7 @@ struct Library {
     decltype(&te_last_error_message) last_error_message;
 } lib{};
 PyObject* error_class = nullptr;      // TeFp8Error(status, message)
+PyObject* memory_error = nullptr;    // torch.OutOfMemoryError
 PyObject* current_stream = nullptr;   // device index -> stream handle
 
 struct Refusal {
@@ -77,7 +78,7 @@ PyObject* guarded(F body)
             Py_DECREF(args);
         }
     } catch (const c10::OutOfMemoryError& e) {
-        PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+        PyErr_SetString(memory_error, e.what_without_backtrace());   // (as torch.empty)
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {
@@ -455,17 +456,17 @@ PyObject* grad_norm_clip(PyObject*, PyObject* const* v, Py_ssize_t n)
     });
 }
 
-// (error class, current stream's function, addresses of the C functions in Library's order)
+// (error class, torch's out-of-memory class, current stream's function, addresses of the C functions in Library's order)
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n)
 {
     constexpr Py_ssize_t kFunctions = sizeof(Library) / sizeof(void*);
-    if (n != 2 + kFunctions) {
+    if (n != 3 + kFunctions) {
         PyErr_SetString(PyExc_TypeError, "bind: wrong number of arguments");
         return nullptr;
     }
     void* at[kFunctions];
     for (Py_ssize_t i = 0; i < kFunctions; ++i) {
-        at[i] = PyLong_AsVoidPtr(v[2 + i]);
+        at[i] = PyLong_AsVoidPtr(v[3 + i]);
         if (!at[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: null function");
             return nullptr;
@@ -475,7 +476,9 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n)
     Py_INCREF(v[0]);
     Py_XSETREF(error_class, v[0]);
     Py_INCREF(v[1]);
-    Py_XSETREF(current_stream, v[1]);
+    Py_XSETREF(memory_error, v[1]);
+    Py_INCREF(v[2]);
+    Py_XSETREF(current_stream, v[2]);
     Py_RETURN_NONE;
 }
 

@@ -4,8 +4,8 @@ norm with clipping.
 
 Signatures and documentation only: the checks of the tensors, the allocation of outputs and the call
 of the C function are native (``csrc/binding.cpp``), and every step of the computation runs in the
-HIP kernels of ``libte_fp8.so``.  A refused call raises ``TeFp8Error`` and launches nothing; without
-the built libraries every call raises.
+HIP kernels of ``libte_fp8.so``.  A refused call raises ``TeFp8Error`` and launches nothing, one whose
+outputs find no memory ``torch.OutOfMemoryError``; without the built libraries every call raises.
 """
 from __future__ import annotations
 
@@ -67,7 +67,7 @@ def _load():
     spec.loader.exec_module(native)
     # (PyTorch's plain handle of the current stream, where it has one: the Stream object around it costs as
     # much as a launch)
-    native.bind(_te.TeFp8Error, getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream),
+    native.bind(_te.TeFp8Error, torch.OutOfMemoryError, getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream),
                 *[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in
                   ("te_rmsnorm_fwd", "te_rmsnorm_bwd", "te_rmsnorm_bwd_workspace_bytes", "te_moe_router_fwd",
                    "te_moe_router_bwd", "te_moe_router_workspace_bytes", "te_grad_norm_clip",
