@@ -150,5 +150,6 @@ def te_grad_norm_clip(grads, max_norm, out=None, norm=None, workspace=None, stre
     if out is not None and type(out) is not list:
         out = list(out)
     if not grads and norm is None:
-        norm = torch.empty((1,), dtype=torch.float32, device="cuda")
+        with torch.cuda.stream(stream):      # (None: the current one)
+            norm = torch.empty((1,), dtype=torch.float32, device="cuda")
     return _call("grad_norm_clip", stream, grads, max_norm, out, norm, workspace)

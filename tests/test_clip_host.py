@@ -5,6 +5,7 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 te = pytest.importorskip("fp8_linear_layer_amd")
@@ -84,3 +85,32 @@ def test_second_pass_starts_where_the_first_ended(recorder):
     sums, scales = split(recorder([1000 + i for i in range(500)]))
     assert [x.first_count for x in scales] == [x.first_count for x in reversed(sums)]
     assert len(sums) == 6
+
+
+def test_an_empty_lists_norm_belongs_to_the_given_stream(monkeypatch):
+    """Without gradients the norm is allocated here: for the stream that writes it, like every other output."""
+    current, seen = ["default"], []
+
+    class Stream:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.s or current[0]
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Native:
+        @staticmethod
+        def grad_norm_clip(grads, max_norm, out, norm, workspace):
+            seen.append(("call", current[0]))
+            return norm
+
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: seen.append(("empty", current[0])) or empty(1))
+    monkeypatch.setattr(ops, "_native", Native)
+    te.te_grad_norm_clip([], 1.0, stream="side")
+    te.te_grad_norm_clip([], 1.0)
+    assert seen == [("empty", "side"), ("call", "side"), ("empty", "default"), ("call", "default")]
