@@ -477,13 +477,23 @@ bool past_caches(int64_t bytes) { return bytes >= (int64_t)128 << 20; }
 
 template <class X, class H, Out kOut> struct Fwd {
     template <int kTPR, int kNV> struct Rows {
+        // Rows of 4097 to 8192 columns take two chunks for each of 512 threads, though 1024 would have one each: from
+        // 1024 rows on two are up to 30 % faster where 1024 threads are half idle, and still 3 to 10 % at 7936
+        // columns (bf16 with the residual, microseconds with one chunk and with two: 4096 x 5120 33.6 and 28.0,
+        // 4096 x 7168 44.0 and 38.8, 2114 x 7936 26.3 and 24.8); few rows take 0.1 to 0.2 us more. At 8192 columns,
+        // where no thread is idle, they are even (4096 x 8192 46.9 and 46.0) but for fp32 x with a residual (with
+        // an fp32 residual 106.7 and 113.9, with a bf16 one 55.2 and 58.4), which keeps one chunk there.  The backward
+        // pass gains nothing from two.
+        static constexpr bool kWide = kTPR == 1024 && kNV == 1, kFullRows = __is_same(X, F32) && !__is_same(H, NoResidual);
         static void run(const NormFwdArgs& a, hipStream_t stream)
         {
-            // (of 1024 threads a row of up to 7168 columns leaves too many without work: two chunks for each of
-            // 512 take 27.8 us for 3276 x 5120 bf16 instead of 31.1, but 29.8 for 2048 x 8192 instead of 28.3;
-            // the backward pass gains nothing)
-            if constexpr (kTPR == 1024 && kNV == 1)
-                if (a.cols <= 7168) return Rows<512, 2>::run(a, stream);
+            if constexpr (!kWide || kFullRows) {
+                if (!kWide || a.cols > 7936) return launch(a, stream);
+            }
+            if constexpr (kWide) Rows<512, 2>::launch(a, stream);
+        }
+        static void launch(const NormFwdArgs& a, hipStream_t stream)
+        {
             constexpr int kThreads = kThreadsOf<kTPR>, kRows = kThreads / kTPR;
             // (a launch has at most 2^32 threads: more rows than that take several)
             constexpr int64_t kMost = ((int64_t)1 << 31) / kThreads * kRows;
