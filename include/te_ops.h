@@ -139,9 +139,9 @@ te_status_t te_moe_router_bwd(const void* logits, te_dtype_t logits_dtype, int64
  *  tensors       host array of n descriptors, read during the call; each tensor
  *                has `count` elements (at most 2^36) one after the other, aligned
  *                to an element.  out may be grad itself (same type: in place, and not
- *                touched where the norm is at most max_norm) or null (only its
- *                part of the norm); apart from that no output overlaps a gradient
- *                or another output
+ *                touched where the coefficient is 1, as it is for a norm of at most
+ *                max_norm - 1e-6) or null (only its part of the norm); apart from
+ *                that no output overlaps a gradient or another output
  *  max_norm      > 0
  *  norm          [1] fp32
  *  workspace     16-byte aligned, te_grad_norm_workspace_bytes(n) bytes

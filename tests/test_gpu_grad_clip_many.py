@@ -74,3 +74,13 @@ def test_graph():
         eager = te.te_grad_norm_clip(grads, 0.01, out=outs)
         torch.cuda.synchronize()
         assert torch.equal(eager, replayed) and torch.equal(out, got), i
+
+
+@pytest.mark.parametrize("max_norm,touched", [(1.0, True), (1.0 + 2.0 ** -21, True), (1.0 + 2.0 ** -19, False), (2.0, False)])
+def test_in_place_is_rewritten_where_the_coefficient_is_below_one(max_norm, touched):
+    """A norm of 1 against limits at and just above it: 1e-6 is added to the norm before the division."""
+    g = torch.zeros(9000, device="cuda")
+    g[17] = 1.0
+    norm = te.te_grad_norm_clip([g], max_norm)
+    coef = torch.tensor(max_norm) / (torch.tensor(1.0) + torch.tensor(1e-6))
+    assert float(norm) == 1.0 and float(g[17]) == min(1.0, float(coef)) and (float(g[17]) < 1.0) == touched
