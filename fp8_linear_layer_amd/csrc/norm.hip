@@ -9,8 +9,8 @@
 // Memory-bound.  A row is read once into registers, eight consecutive columns (16 bytes
 // of bf16) per thread and as many threads as the row needs; the row's sum of squares is reduced
 // over the wave by lane exchanges and over the waves through LDS, and everything that follows
-// works from the registers.  Sixteen consecutive lanes hold one 128-column group, so the fp8 cast
-// needs a four-step lane exchange and no LDS.
+// works from the registers (but for the backward pass beyond 16384 columns, which reads the row again).
+// Sixteen consecutive lanes hold one 128-column group, so the fp8 cast needs a four-step lane exchange and no LDS.
 //
 // Rows whose length is no multiple of eight: the last chunk starts at cols - 8 and overlaps its
 // neighbour; the columns that the neighbour has too are left out of the sums and written twice
@@ -20,8 +20,8 @@
 // The cast of the transpose has groups of 128 rows and needs the rstd of each of them, so it runs
 // as a second kernel over 128 x 64 tiles of the stored h.
 //
-// Measured at 8192 x 4096 bf16 with the residual: forward into fp8 42.3 us (235 MB, 5.6 TB/s), the transposed cast
-// 17.6 us (101 MB, 5.7 TB/s), backward 46.7 us (277 MB, 5.9 TB/s) and 5.0 us for the sums.
+// Measured at 8192 x 4096 bf16 with the residual: forward into fp8 45.6 us (235 MB, 5.2 TB/s), the transposed cast
+// 18.2 us (101 MB, 5.5 TB/s), backward 47.1 us (277 MB, 5.9 TB/s) and 5.1 us for the sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -304,7 +304,8 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void rmsnorm_bwd_kernel(const Nor
 {
     constexpr int kRows = kThreadsOf<kTPR> / kTPR;
     // Four chunks per thread do not fit the registers beside the sums for dgamma: such rows are read again
-    // after the reduction (838 x 20000 bf16: 150 us with the registers spilled).
+    // after the reduction (838 x 20000 bf16: 45 us, and 150 with all of it kept and the registers spilled).  With
+    // an fp32 operand 3 to 25 registers are spilled all the same (838 x 20000 in fp32: 101 us).
     constexpr bool kTwice = kNV == 4;
     __shared__ float red[2][kThreadsOf<kTPR> / 64];
     __shared__ float slots[kRows > 1 ? kRows : 1][kRows > 1 ? kTPR * 8 : 1];
@@ -468,11 +469,15 @@ int threads_per_row(int64_t cols)
     return cols <= 128 ? 16 : cols <= 256 ? 32 : cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
 }
 
-// Inputs of this many bytes are read past the caches, so that h and the outputs stay in the last one.  Forward
-// with the residual, 4096 columns of bf16, fp8 output, inputs that were not used just before: 8192 rows (128
-// MiB) 47.1 us ordinarily and 45.1 past the caches with four sets of inputs in turn, 51.7 and 40.0 with two; 2048
-// rows 12.2 and 14.0; 8192 rows of the same inputs again and again (still in the cache) 35.0 and 41.0.  The
-// backward pass is slower that way at every size (8192 rows: 55.5 and 60.3).
+// Inputs of this many bytes are read past the caches, so that h and the outputs stay in the last one: with them a
+// call of this size fills its 256 MiB.  Forward with the residual, 4096 columns of bf16, without the transposed cast,
+// ordinarily and past the caches, in microseconds: where x was just written by another kernel and the residual was not
+// touched lately, 96 MiB 32.2 and 31.6, 128 MiB 48.1 and 40.5, 160 MiB 53.2 and 51.3, 256 MiB 96.7 and 82.4, 512 MiB
+// 176.7 and 159.5; where neither was touched lately, 33.0 and 33.0, 46.7 and 40.3, 56.1 and 50.3, 110.4 and 77.8,
+// 179.3 and 182.7; of the same inputs again and again (still in the cache where they fit), 29.8 and 33.0, 38.8 and
+// 41.8, 55.7 and 50.1, 107.2 and 79.4, 180.2 and 184.7.  From 64 MiB down they differ by at most 2 us either way.  The
+// residual alone past the caches lies between the two.  The backward pass is slower that way at every size (8192 rows:
+// 55.5 and 60.3).
 bool past_caches(int64_t bytes) { return bytes >= (int64_t)128 << 20; }
 
 template <class X, class H, Out kOut> struct Fwd {

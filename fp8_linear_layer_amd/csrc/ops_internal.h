@@ -16,7 +16,7 @@ te_status_t report_ok();
 bool log_calls();
 
 // ------------------------------------------------------------ root-mean-square norm
-constexpr int kNormMaxCols = 32768;   // a row stays in the registers of one workgroup
+constexpr int kNormMaxCols = 32768;   // a row fits the registers of one workgroup (forward)
 enum class NormOut : int { Bf16, F32, Fp8 };
 
 struct NormFwdArgs {

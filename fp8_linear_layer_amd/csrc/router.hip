@@ -20,9 +20,10 @@
 // once, as one row of the workspace that a second kernel adds up in a fixed order.  Calls of few
 // tokens run in one workgroup that finishes by itself.
 //
-// Measured at 65536 tokens, 256 experts, bf16, top 8: forward 19.9 us and 4.9 us for the second kernel, bound by
-// its vector instructions (~930 per eight tokens; 38 MB would take 7.2 us); backward 13.5 us, bound by
-// memory (71 MB at 5.3 TB/s).
+// Measured at 65536 tokens, 256 experts, bf16, top 8: forward 19.7 us and 4.8 us for the second kernel (38 MB
+// would take 7.2 us).  The first issues 918 vector instructions per wave and step of eight tokens, 13 to 14 us of it by
+// their cycles; the rest is waiting, with two waves on a SIMD and no loads ahead of the step.  Backward 13.7
+// us, bound by memory (71 MB at 5.2 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -780,9 +781,10 @@ template <class T> hipError_t bwd_shape(const RouterBwdArgs& a, hipStream_t stre
 }  // namespace
 
 // Workgroups: one where it takes the tokens in at most four steps and the counts are asked for (no second
-// kernel then).  Else as many as are resident, and with four chunks per lane half of that: those are bound
-// by their instructions, and every workgroup costs the second kernel a row (16384 x 512 bf16, both kernels: 17.1
-// us with 256 workgroups, 19.6 with 512; 100000 x 64 fp32: 30.2 and 27.3).
+// kernel then).  Else as many as are resident, and with four chunks per lane half of that: their time is mostly
+// instructions, and every workgroup costs the second kernel a row (both kernels with 256 workgroups and with 512:
+// 65536 x 256 bf16 23.4 and 24.6 us, 16384 x 512 bf16 17.3 and 18.7, 32768 x 256 fp32 23.1 and 27.3; 100000 x 64 fp32
+// 30.5 and 27.3, 100000 x 100 fp32 41.5 and 37.2).
 int64_t router_fwd_blocks(int64_t tokens, int64_t experts, bool loss)
 {
     const Shape s = shape_of(experts);
