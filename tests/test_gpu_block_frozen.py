@@ -60,3 +60,15 @@ def test_norm():
         grads.append(x.grad)
         assert bool((m.weight.main_grad != 0).any()) == train
     assert torch.equal(*grads)
+
+
+def test_create_graph():
+    """First gradients with the graph kept are the plain ones, and differentiating them again raises."""
+    m = block.RmsNorm(256, main_grad=False)
+    x = randn((8, 256), 1).requires_grad_()
+    dy = randn((8, 256), 2)
+    plain = torch.autograd.grad(m(x)[0], [x, m.weight], dy)
+    first = torch.autograd.grad(m(x)[0], [x, m.weight], dy, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(plain, first))
+    with pytest.raises(RuntimeError, match="second derivative"):
+        first[0].float().square().sum().backward()
