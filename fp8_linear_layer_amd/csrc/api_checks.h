@@ -31,6 +31,15 @@ constexpr int64_t kMaxRows = (int64_t)1 << 31;
     return TE_OK;
 }
 
+// An output [..][ld] that may be an input's own buffer: at another row stride its rows would be written over rows that
+// are still to be read.
+[[maybe_unused]] te_status_t check_in_place(const char* fn, const void* out, int64_t ld, const void* in, int64_t ld_in, int64_t rows)
+{
+    if (in && out == in && rows > 1 && ld != ld_in)
+        return report(TE_ERR_INVALID_ARGUMENT, "%s: in place needs one row stride (got %lld, %lld)", fn, (long long)ld, (long long)ld_in);
+    return TE_OK;
+}
+
 [[maybe_unused]] te_status_t check_array(const char* fn, const char* what, const void* p, int align = 4)
 {
     if (!p) return report(TE_ERR_INVALID_ARGUMENT, "%s: %s pointer is null", fn, what);

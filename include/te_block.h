@@ -148,7 +148,7 @@ te_status_t te_dropout(const void* x, te_dtype_t x_dtype, int64_t ld_x,
  *  x, residual   TE_DTYPE_BF16 or TE_DTYPE_F32, each on its own
  *  gamma, beta   [cols] bf16; beta may be null (0)
  *  cols          1 .. 32768
- *  h             may be the residual's own buffer (the sum in place)
+ *  h             may be the residual's own buffer (the sum in place; same stride)
  *  mean, rstd    [rows] fp32, for the backward pass
  *  p, rng        dropout of x as te_dropout's; p = 0: none (rng may be null)
  */
@@ -170,7 +170,7 @@ te_status_t te_layernorm_fwd(const void* x, te_dtype_t x_dtype, int64_t ld_x,
  *  dy            TE_DTYPE_BF16 or TE_DTYPE_F32
  *  h             what the norm was of: the stored h, or x without a residual
  *  dres          the gradient that reaches h from elsewhere, h's type, or null
- *  dh            h's type; may be dres's own buffer
+ *  dh            h's type; may be dres's own buffer (same stride)
  *  dx            TE_DTYPE_BF16 or TE_DTYPE_F32, needed with p > 0 (never with 0)
  *  dgamma, dbeta [cols] fp32, overwritten; null: not computed
  *  workspace     16-byte aligned, te_layernorm_bwd_workspace_bytes(rows, cols)
