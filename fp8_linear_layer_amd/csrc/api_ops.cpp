@@ -55,6 +55,7 @@ te_status_t te_rmsnorm_fwd(const void* x, te_dtype_t x_dtype, int64_t ld_x, cons
         if (residual) {
             TE_CHECK(check_matrix(fn, "residual", residual, residual_dtype, ld_residual, cols));
             TE_CHECK(check_matrix(fn, "h", h, residual_dtype, ld_h, cols));
+            TE_CHECK(check_in_place(fn, h, ld_h, residual, ld_residual, rows));
         } else if (h) {
             return report(TE_ERR_INVALID_ARGUMENT, "%s: h given without a residual", fn);
         }
@@ -145,6 +146,7 @@ te_status_t te_rmsnorm_bwd(const void* dy, te_dtype_t dy_dtype, int64_t ld_dy, c
             TE_CHECK(check_matrix(fn, "h", h, h_dtype, ld_h, cols));
             TE_CHECK(check_matrix(fn, "dh", dh, h_dtype, ld_dh, cols));
             if (dres) TE_CHECK(check_matrix(fn, "dres", dres, h_dtype, ld_dres, cols));
+            TE_CHECK(check_in_place(fn, dh, ld_dh, dres, ld_dres, rows));
             TE_CHECK(check_array(fn, "rstd", rstd));
             TE_CHECK(check_array(fn, "gamma", gamma_bf16, 2));
         }

@@ -50,7 +50,7 @@ extern "C" {
  *  x, residual   TE_DTYPE_BF16 or TE_DTYPE_F32, each on its own
  *  gamma         [cols] bf16
  *  cols          1 .. 32768
- *  h             may be the residual's own buffer (the sum in place)
+ *  h             may be the residual's own buffer (the sum in place; same stride)
  *  rstd          [rows] fp32, for the backward pass
  *  cast_flags    0 or TE_CAST_POW2_SCALE
  */
@@ -70,7 +70,7 @@ te_status_t te_rmsnorm_fwd(const void* x, te_dtype_t x_dtype, int64_t ld_x,
  *  dy            TE_DTYPE_BF16 or TE_DTYPE_F32
  *  h             what the norm was of: the stored h, or x without a residual
  *  dres          the gradient that reaches h from elsewhere, h's type, or null
- *  dh            h's type; may be dres's own buffer
+ *  dh            h's type; may be dres's own buffer (same stride)
  *  dgamma        [cols] fp32, overwritten; null: not computed
  *  workspace     16-byte aligned, te_rmsnorm_bwd_workspace_bytes(rows, cols)
  *                bytes (contents irrelevant; unused without dgamma)

@@ -39,3 +39,16 @@ def test_layernorm_fwd(lib, rows, ld_res, ld_h, dtype):
 def test_layernorm_bwd(lib, rows, ld_res, ld_dh, p):
     drop = (p, G, T, BF, 256) if p else (0.0, None, None, BF, 0)
     refused(lib, lib.te_layernorm_bwd(A, BF, 256, B, BF, 256, C, C, D, rows, 256, S, ld_res, S, ld_dh, *drop, None, None, None, 0, None))
+
+
+@pytest.mark.parametrize("ld_res,ld_h", [(256, 264), (264, 256), (512, 256)])
+@pytest.mark.parametrize("rows", [2, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rmsnorm_fwd(lib, rows, ld_res, ld_h, dtype):
+    refused(lib, lib.te_rmsnorm_fwd(A, BF, 256, S, dtype, ld_res, B, 1e-5, rows, 256, S, ld_h, C, D, BF, 256, 0, None, None, 0, None, None))
+
+
+@pytest.mark.parametrize("ld_res,ld_dh", [(256, 264), (264, 256), (512, 256)])
+@pytest.mark.parametrize("rows", [2, 128])
+def test_rmsnorm_bwd(lib, rows, ld_res, ld_dh):
+    refused(lib, lib.te_rmsnorm_bwd(A, BF, 256, B, BF, 256, C, D, rows, 256, S, ld_res, S, ld_dh, None, None, 0, None))
