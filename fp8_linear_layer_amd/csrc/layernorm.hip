@@ -345,7 +345,8 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void layernorm_bwd_kernel(const L
                 const float p = dyv[j] * ((hv[j] - mu) * rs);
                 dg[i][j] += in ? p : 0.0f;
                 db[i][j] += in ? dyv[j] : 0.0f;
-                const bool mine = c[i].on && j >= c[i].skip;
+                // (behind the end of a row of less than eight columns p may be 0 times an overflow)
+                const bool mine = c[i].on && j >= c[i].skip && (kTPR > 16 || cols >= 8 || j < cols);
                 sg += mine ? dyv[j] * g[j] : 0.0f;
                 sx += mine ? p * g[j] : 0.0f;
             }
