@@ -1,5 +1,7 @@
 // The Python side of a gated block's operators (te_block.h): checks what the C ABI cannot see of a tensor, allocates
 // the outputs that are not given, and calls the C function, as binding.cpp does for te_ops.h.
+#include <limits>
+
 #include "binding_util.h"
 #include "te_block.h"
 
@@ -39,6 +41,9 @@ const int64_t* state(const at::Tensor& rng, double p, const at::Device& device)
     array(rng, "rng", at::kLong, {2}, device);
     return static_cast<const int64_t*>(rng.data_ptr());
 }
+
+// The rate as the C functions take it.  One that is too small for fp32 drops nothing, but is not 0: outputs go by that.
+float rate(double p) { return p > 0.0 ? std::max((float)p, std::numeric_limits<float>::min()) : 0.0f; }
 
 // The outputs of a call that stores bf16 / fp32 (y) or fp8 in one or both layouts.
 struct Result {
@@ -166,7 +171,7 @@ PyObject* layernorm_fwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         make_or_check(rstd, "rstd", kF32, {rows}, device);
         const Result r = result(v + 14, out, rowwise, transpose, rows, cols, device, "y");
         check(lib.layernorm_fwd(ptr(x), type_of(x), ld_x, ptr(residual), residual.defined() ? type_of(residual) : TE_DTYPE_BF16, ld_res,
-                                (float)p, from, ptr(gamma), ptr(beta), (float)eps, rows, cols, ptr(h), ld_h, ptr<float>(mean),
+                                rate(p), from, ptr(gamma), ptr(beta), (float)eps, rows, cols, ptr(h), ld_h, ptr<float>(mean),
                                 ptr<float>(rstd), r.first(), (te_dtype_t)out, r.ld, (uint32_t)flags, ptr<float>(r.scales), ptr(r.qt), r.ld_qt,
                                 ptr<float>(r.scales_t), stream_of(device)));
         return tuple_of({h, mean, rstd, r.y, r.q, r.scales, r.qt, r.scales_t});
@@ -210,7 +215,7 @@ PyObject* layernorm_bwd(PyObject*, PyObject* const* v, Py_ssize_t n)
         if (need_dbeta) make_or_check(dbeta, "dbeta", kF32, {cols}, device);
         if (need_dgamma || need_dbeta) workspace_for(workspace, lib.layernorm_bwd_workspace_bytes(rows, cols), device);
         check(lib.layernorm_bwd(ptr(dy), type_of(dy), ld_dy, ptr(h), type_of(h), ld_h, ptr<float>(mean), ptr<float>(rstd), ptr(gamma), rows,
-                                cols, ptr(dres), ld_res, ptr(dh), ld_dh, (float)p, from, ptr(dx), (te_dtype_t)dx_type, ld_dx,
+                                cols, ptr(dres), ld_res, ptr(dh), ld_dh, rate(p), from, ptr(dx), (te_dtype_t)dx_type, ld_dx,
                                 ptr<float>(dgamma), ptr<float>(dbeta), ptr(workspace), bytes(workspace), stream_of(device)));
         return tuple_of({dh, dx, dgamma, dbeta});
     });
@@ -235,7 +240,7 @@ PyObject* dropout(PyObject*, PyObject* const* v, Py_ssize_t n)
         if (type != TE_DTYPE_BF16 && type != TE_DTYPE_F32) refuse("out_dtype: expected TE_DTYPE_BF16 or TE_DTYPE_F32");
         const int64_t ld_out = make_or_check_rows(out, "out", type == TE_DTYPE_BF16 ? kBf16 : kF32, shape, device);
         check(lib.dropout(ptr(x), type_of(x), ld_x, ptr(residual), residual.defined() ? type_of(residual) : TE_DTYPE_BF16, ld_res, shape[0],
-                          shape[1], (float)p, from, ptr(out), (te_dtype_t)type, ld_out, stream_of(device)));
+                          shape[1], rate(p), from, ptr(out), (te_dtype_t)type, ld_out, stream_of(device)));
         return wrap(out);
     });
 }

@@ -1,5 +1,6 @@
 """Edges of te_layernorm_fwd / te_layernorm_bwd that test_gpu_layernorm leaves out: rows of less than eight columns far from
-zero, fp8 outputs of one group, and long rows of which a workgroup of the backward pass has several.  Tolerances as there."""
+zero, fp8 outputs of one group, long rows of which a workgroup of the backward pass has several, and rates below fp32's
+smallest.  Tolerances as there."""
 import numpy as np
 import pytest
 import torch
@@ -77,3 +78,23 @@ def test_backward_of_many_long_rows(cols, yt, ht, dres, p):
         mine = args[5].clone()
         got = te.te_layernorm_bwd(*args[:5], dres=mine, p=p, rng=rng() if p else None, dh=mine, dx_dtype=OUT[yt])
         assert torch.equal(mine, r.dh) and torch.equal(got.dgamma, r.dgamma) and (not p or torch.equal(got.dx, r.dx))
+
+
+@pytest.mark.parametrize("p", [1e-30, 1e-46, 1e-300])
+def test_rates_too_small_for_fp32(p):
+    """Such a rate drops nothing, as any below 2^-17, and the calls and the modules take it all the same."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, res, dy = (normal(g, (9, 72), torch.bfloat16) for _ in range(3))
+    gamma = vector(g, 72, 0.1, 1.0)
+    want = te.te_layernorm_fwd(x, gamma, None, EPS, residual=res)
+    r = te.te_layernorm_fwd(x, gamma, None, EPS, residual=res, p=p, rng=rng())
+    assert torch.equal(r.h, want.h) and torch.equal(r.y, want.y)
+    b, plain = te.te_layernorm_bwd(dy, r.h, r.mean, r.rstd, gamma, p=p, rng=rng()), te.te_layernorm_bwd(dy, r.h, r.mean, r.rstd, gamma)
+    assert torch.equal(b.dh, plain.dh) and torch.equal(b.dx, plain.dh)
+    assert torch.equal(te.te_dropout(x, p, rng()), x)
+    from fp8_linear_layer_amd import block
+    m = block.LayerNorm(72, dropout=p, seed=1)
+    xs, rs = x.clone().requires_grad_(), res.clone().requires_grad_()
+    y, _ = m(xs, rs)
+    y.backward(dy)
+    assert torch.equal(xs.grad, rs.grad) and (xs.grad != 0).any()
