@@ -280,6 +280,11 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void layernorm_bwd_kernel(const L
     constexpr int kRows = kThreadsOf<kTPR> / kTPR;
     // (rows of more than 16384 columns are read again after the reduction, as in norm.hip)
     constexpr bool kTwice = kNV == 4;
+    // The next row's loads are out before this row's sums, where a thread has one chunk (8192 x 4096 without dropout 51.2 us,
+    // and 55.3 without that).  With two the registers do not hold two rows (spilled, 2048 x 8200 bf16 182 us, and 130
+    // without; 8192 x 14336 721 and 471; fp32 1099 and 627), and rows that are read twice gain nothing from their mean
+    // and deviation alone (4096 x 32768 878 and 861, fp32 1117 and 975).
+    constexpr bool kAhead = kNV == 1;
     __shared__ float2 red[2][kThreadsOf<kTPR> / 64];
     __shared__ float slots[kRows > 1 ? kRows : 1][kRows > 1 ? kTPR * 8 : 1];
     const int t = threadIdx.x % kTPR, slot = threadIdx.x / kTPR, cols = a.cols;
@@ -294,7 +299,6 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void layernorm_bwd_kernel(const L
         for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
     }
     const DropKey key = drop_key(a.drop);
-    // (the next row's loads are out before this row's sums: 8192 x 4096 without dropout 51.2 us, and 55.3 without that)
     Raw8<Y> ry[kNV];
     Raw8<H> rh[kNV], rr[kNV];
     float mean, rstd;
@@ -310,13 +314,14 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void layernorm_bwd_kernel(const L
     };
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t base = (int64_t)blockIdx.x * kRows;
-    load(base);
+    if constexpr (kAhead) load(base);
     for (int parity = 0; base < a.rows; base += step, parity ^= 1) {
         const bool in = kRows == 1 || base + slot < a.rows;
         const int64_t row = in ? base + slot : a.rows - 1;
         const auto* dy = static_cast<const typename Y::store_t*>(a.dy) + row * a.ld_dy;
         const auto* h = static_cast<const typename H::store_t*>(a.h) + row * a.ld_h;
         const auto* res = static_cast<const typename H::store_t*>(a.dres) + (kRes ? row * a.ld_dres : 0);
+        if constexpr (!kAhead) load(base);
         // (what this row needs of the loads, before the next row's take their registers)
         Raw8<Y> cy[kNV];
         Raw8<H> ch[kNV], cr[kNV];
@@ -327,7 +332,8 @@ __global__ __launch_bounds__(kThreadsOf<kTPR>) void layernorm_bwd_kernel(const L
             ch[i] = rh[i];
             if constexpr (kRes) cr[i] = rr[i];
         }
-        if (base + step < a.rows) load(base + step);
+        if constexpr (kAhead)
+            if (base + step < a.rows) load(base + step);
         float sg = 0.0f, sx = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
