@@ -2,6 +2,8 @@
 below 64 MiB, more rows than one launch has, the longest rows in the transposed layout; and the gated modules without a graph.
 
 Tolerances: those of test_gpu_gated and test_gpu_layernorm."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -21,6 +23,14 @@ def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     te.load_library()
+    # (what the products' library keeps for itself is allocated now, not inside one of the gigabytes that follow, which
+    # could then not be given back)
+    one = torch.ones((64, 64), dtype=torch.float64, device="cuda")
+    torch.cuda.synchronize()
+    one @ one
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("rows", [1, 130])
