@@ -90,7 +90,11 @@ enum class Act : int { Silu = 1, Gelu = 2 };
 //   forward:  out (y, plain), q_out / q_scales / qt_out / qt_scales (y, fp8), aux (z, or null)
 //   dgrad:    out (dz, plain), q_out ... (dz, fp8), preact (z)
 // and flags = the activation.
-constexpr int64_t kFewRows = 128;   // most rows of the kernel for few tokens
+// Most rows of the kernel for few tokens, whose sums are exact but for fp32 roundings in any batch of up to so many.  It is
+// not always the faster one (us by it and by the parts of gated.hip, K -> H, at 16, 32, 64
+// and 128 rows): 7168 -> 2048 12.2, 29.0; 14.5, 29.5; 20.5, 31.4; 21.3, 30.9.  2048 -> 1024 4.5, 10.3; 5.7, 10.4; 8.4, 10.5; 8.7,
+// 10.6.  4096 -> 7168 16.6, 20.1; 19.8, 20.5; 28.4, 21.7; 37.4, 21.7.  4096 -> 14336 27.3, 31.8; 33.4, 30.7; 41.6, 30.8; 62.9, 39.1.
+constexpr int64_t kFewRows = 128;
 // Whether the row-wise cast of y reads fp32 rows that the large products' kernels left in the workspace.
 bool gated_fwd_through_f32(int64_t M, int64_t H);
 hipError_t launch_gated_fwd(const GemmArgs& a, hipStream_t stream);

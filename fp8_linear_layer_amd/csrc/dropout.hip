@@ -3,8 +3,8 @@
 // Elementwise over chunks of eight columns (one counter of the generator each); a workgroup takes 1024 chunks that
 // follow each other, four to a thread, whose loads are all in flight before the first is used.  The row's end that
 // fills no chunk goes element by element.  A thread reads its chunks before it writes them and nobody else's, so out
-// may be x's or the residual's buffer.  Memory-bound, generator and all: 8192 x 4096 bf16 with the residual 33.7 us (201 MB,
-// 6.0 TB/s) with p = 0.1 and 33.5 with p = 0; without the residual 23.6 us.
+// may be x's or the residual's buffer.  Memory-bound, generator and all: 8192 x 4096 bf16 with the residual 33.4 us (201 MB,
+// 6.0 TB/s) with p = 0.1 and 33.1 with p = 0; without the residual 23.2 and 21.3.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -13,9 +13,10 @@
 // Formulas: with s = 1 / (1 + exp(-u)), u = g (SiLU) or 2 c (g + a g^3) (the tanh form of GELU),
 //   act = g s,  act' = s (1 + g (1 - s) u')
 //
-// 8192 rows, 4096 -> 14336, SiLU: forward with z 969 us (1.99 PFLOP/s; gemm.hip's plain product of that size 1000 us: the
-// epilogue hides), data gradient to e5m2 in both layouts 686 us: 500 of products at that rate, and the 940 MB of z and dz
-// behind each tile, where every workgroup asks memory at once.
+// 8192 rows, 4096 -> 14336, SiLU: forward with z in bf16 1008 us (1.91 PFLOP/s; gemm.hip's plain product of that size 1001:
+// the epilogue hides), in e4m3 in both layouts 1063; with FAST on power-of-two scales 896 and 941 (the plain product 882).
+// Data gradient to e5m2 in both layouts 709 us: 496 of products (gemm.hip's of that size), and the 940 MB of z and dz behind
+// each tile, where every workgroup asks memory at once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -899,6 +900,12 @@ namespace {
 //                         512 x 24576 (6) 86.5, 107.9;  2048 x 8192 (8) 93.4, 151.9
 //   forward, bf16         512 x 8192 49.8, 27.3;  300 x 16384 51.2, 38.6;  512 x 16384 52.2, 49.5;  512 x 24576 64.9, 87.1
 //   forward, fp8          512 x 8192 51.7, 31.2;  512 x 12288 (3) 51.8, 45.1;  512 x 16384 52.3, 55.8
+// At four parts a unit short contractions gain a little by it and long ones lose as much:
+//   K = 1024, bf16        data gradient 512 x 8192 30.6, 15.5;  512 x 16384 32.3, 26.8;  512 x 24576 47.4, 46.4
+//                         forward 19.4, 11.5;  21.0, 20.3;  23.1, 27.2
+//   K = 14336, bf16       data gradient 194, 111;  200, 212;  228, 313;  forward 178, 105;  181, 199;  210, 295
+// The cast of the transpose needs 128 rows and a part has 64, so it takes tiles however few: 512 rows, forward 512 x 8192
+// with z 56 us (row-wise alone 32), data gradient 81 (31).
 bool by_parts(int64_t M, int64_t N, int most = 4)
 {
     return ((M + kWM - 1) / kWM) * ((N + kWN - 1) / kWN) <= (int64_t)most * device_cus();

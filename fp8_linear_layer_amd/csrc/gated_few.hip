@@ -291,9 +291,12 @@ __global__ __launch_bounds__(kFinishThreads) void gated_finish_transpose_kernel(
         *reinterpret_cast<const uint4*>(codes + (t >> 3) * kLd + (t & 7) * 16);
 }
 
-// Weights of this many bytes go past the caches, where one group of rows reads them: of 117 MB each, and others in
-// between (more than the last cache holds), one token takes 25.7 us so and 27.3 through them; of 34 MB each, which the
-// last cache still holds, 9.1 and 8.9, of 29 MB 11.1 and 7.7.
+// Weights of this many bytes go past the caches where 16 rows or less read them, which supposes that other weights are read
+// between two calls, as in a model of several layers.  One row, us past the caches and through them, for weights in turn
+// that together are more than the last cache (256 MiB) holds, and for the same weights again at once: 56 MiB 15.0, 15.3 and
+// 13.7, 12.3; 84 MiB 20.0, 21.5 and 18.8, 16.4; 112 MiB 25.4, 27.4 and 24.0, 20.2; 224 MiB 45.3, 48.5 and 44.5, 39.7; 448 MiB
+// 88.5, 92.7 and 91.8, 94.4.  More rows gain less by it than the same weights again would lose: 112 MiB, 32 rows 30.5, 31.6
+// and 29.6, 22.3; 64 rows 40.2, 40.6 and 39.9, 33.3.
 constexpr int64_t kPastBytes = (int64_t)96 << 20;
 
 template <int kFmtA, int kFmtB>

@@ -10,10 +10,13 @@
 // corrected for that rounding, takes a second reduction.  Dropout's bits are computed in registers, one counter of
 // the generator per chunk.
 //
-// Memory-bound: x, residual, h and y once each.  8192 x 4096 bf16 with the residual to e4m3: 46.6 us, with dropout 52.0
+// Memory-bound: x, residual, h and y once each.  8192 x 4096 bf16 with the residual to e4m3: 49 us, with dropout 51
 // (the generator's multiplications, in a kernel whose one row per workgroup leaves little to hide them behind), with the
-// transposed layout as well 69.9, whose second kernel reads h once more; to fp32 without a residual, 4999 x 2112, 15.5 us
-// (5.4 TB/s).  Backward, 8192 x 4096: 50.3 us, with dropout 72.1.
+// transposed layout as well 64 and 68, whose second kernel reads h once more; to fp32 without a residual, 4999 x 2112, 16.4 us
+// (5.1 TB/s).  Backward, 8192 x 4096: 44.6 us, with dropout 53.8; with the residual's gradient 57 and 75.
+// Rows of more than 8192 columns take 1024 threads of 128 registers.  They hold the forward's chunks up to 16384 columns (8192 x
+// 14336 with the residual to bf16 217 us, the root-mean-square norm's 173) and spill some beyond (4096 x 32768 250 and 206);
+// the backward's two column sums do not fit beside its chunks (with the residual's gradient 468 and 178; 856 and 254).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

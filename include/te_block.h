@@ -71,7 +71,12 @@ typedef enum {
  *                update).  Up to 128 rows both policies sum the
  *                products of a block exactly but for fp32 roundings (a kernel of
  *                their own, on bf16 copies of the codes); otherwise with the
- *                precision of the matrix cores' fp8 sums.
+ *                precision of the matrix cores' fp8 sums (about 1.5e-5 of the
+ *                terms' size, as in the GEMMs of te_fp8.h).  FAST's power-of-two test is
+ *                taken per tile of the kernel that runs, and the outputs that are
+ *                asked for choose that kernel: on scales of which only some are
+ *                powers of two, results may differ between such calls within
+ *                that precision.  Under FULL they do not.
  */
 int64_t te_fp8_gated_fwd_workspace_bytes(int64_t M, int64_t H, int64_t K, te_dtype_t y_dtype);
 te_status_t te_fp8_gated_fwd(const void* x, const float* x_scales, te_dtype_t x_dtype,
@@ -94,7 +99,8 @@ te_status_t te_fp8_gated_fwd(const void* x, const float* x_scales, te_dtype_t x_
  *  dy, dy_scales [M][K] fp8, [K/128][te_scale_ld(M)] fp32
  *  wt, wt_scales [H][K] fp8, [K/128][te_scale_ld(H)] fp32
  *  z_bf16        [M][ld_z] bf16, the forward's
- *  accum         both policies run TE_ACCUM_FULL_FP32's update
+ *  accum         both policies run TE_ACCUM_FULL_FP32's update, at every M with
+ *                the precision of the matrix cores' fp8 sums
  */
 te_status_t te_fp8_gated_dgrad(const void* dy, const float* dy_scales, te_dtype_t dy_dtype,
                                const void* wt, const float* wt_scales, te_dtype_t wt_dtype,
