@@ -59,7 +59,7 @@ typedef enum {
  *  x, x_scales   [M][K] fp8, [K/128][te_scale_ld(M)] fp32
  *  w, w_scales   [2H][K] fp8, [K/128][te_scale_ld(2H)] fp32
  *  M >= 1;  H, K >= 128, multiples of 128 (H is the contraction length of the
- *                product that reads y); H at most 2^22
+ *                product that reads y); both at most 2^22
  *  z_bf16        [M][ld_z] bf16, the rounded projections for the backward
  *                pass, ld_z >= 2H, or null
  *  ld_y          % 8 == 0 for bf16, % 4 for fp32, % 16 for fp8; ld_z % 8 == 0;
